@@ -26,6 +26,10 @@ HQQ_ERR_ALIGNMENT = 3
 HQQ_ERR_LAUNCH = 4
 HQQ_ERR_TABLE_MISMATCH = 5
 
+HQQ_DTYPE_F16 = 0
+HQQ_DTYPE_BF16 = 1
+HQQ_DTYPE_F32 = 2
+
 # Symbols declared in include/hqq.h.
 EXPORTED_SYMBOLS = ("hqq_quantize", "hqq_quantize_ex", "hqq_quantize_batch", "hqq_dequantize",
                     "hqq_quantize_tensor_stop", "hqq_tensor_stop_workspace_bytes", "hqq_matmul",
@@ -34,7 +38,13 @@ EXPORTED_SYMBOLS = ("hqq_quantize", "hqq_quantize_ex", "hqq_quantize_batch", "hq
                     "hqq_meta_quantize", "hqq_meta_dequantize", "hqq_meta_groups",
                     "hqq_meta_workspace_bytes", "hqq_meta_quantize_batch",
                     "hqq_packed_bytes", "hqq_num_groups", "hqq_status_string",
-                    "hqq_quantize_tensor_stop_noalloc", "hqq_tensor_stop_noalloc_max_bytes")
+                    "hqq_quantize_tensor_stop_noalloc", "hqq_tensor_stop_noalloc_max_bytes",
+                    "hqq_matmul_backward", "hqq_matmul_backward_workspace_bytes",
+                    "hqq_expert_sort", "hqq_expert_sort_workspace_bytes", "hqq_expert_gather",
+                    "hqq_expert_combine", "hqq_expert_combine_backward", "hqq_matmul_experts",
+                    "hqq_matmul_experts_backward", "hqq_matmul_experts_backward_workspace_bytes",
+                    "hqq_adapters", "hqq_adapters_workspace_bytes", "hqq_adapters_backward",
+                    "hqq_adapters_backward_workspace_bytes")
 
 
 class HQQError(RuntimeError):
@@ -107,6 +117,27 @@ def load_library(path: str = LIB_PATH):
                                             P, P, P, P]
     lib.hqq_meta_workspace_bytes.restype = I64
     lib.hqq_meta_workspace_bytes.argtypes = []
+    for name, args in (
+            ("hqq_matmul_backward", [P, I64, I64, P, P, P, I64, I, I, P, I, P, P]),
+            ("hqq_expert_sort", [P, I64, I, I, P, P, P, P, P]),
+            ("hqq_expert_gather", [P, I, I64, I, I64, P, P, P]),
+            ("hqq_expert_combine", [P, I, I64, I, I64, P, P, P, P]),
+            ("hqq_expert_combine_backward", [P, P, I, I64, I, I64, P, P, P, P, P]),
+            ("hqq_matmul_experts", [P, I64, I64, P, I, P, I, P, P, P, I64, I, I, P, I, P]),
+            ("hqq_matmul_experts_backward", [P, I64, I64, P, I, P, P, P, I64, I, I, P, I, P, P]),
+            ("hqq_adapters", [P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P]),
+            ("hqq_adapters_backward", [P, P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P, P,
+                                       P])):
+        getattr(lib, name).restype = I
+        getattr(lib, name).argtypes = args
+    for name, args in (
+            ("hqq_matmul_backward_workspace_bytes", [I64, I64, I64]),
+            ("hqq_expert_sort_workspace_bytes", [I64, I, I]),
+            ("hqq_matmul_experts_backward_workspace_bytes", [I64, I64, I64, I]),
+            ("hqq_adapters_workspace_bytes", [I64, I64, I64, I, I]),
+            ("hqq_adapters_backward_workspace_bytes", [I64, I64, I64, I, I])):
+        getattr(lib, name).restype = I64
+        getattr(lib, name).argtypes = args
     lib.hqq_dequantize.restype = I
     lib.hqq_dequantize.argtypes = [P, P, P, I64, I64, I, I, P, P]
     lib.hqq_packed_bytes.restype = I64
@@ -250,6 +281,92 @@ def hqq_dequantize(packed_codes: int, scale_f16: int, zero_f16: int, rows: int, 
                    nbits: int, group_size: int, W_out_f16: int, stream: int = 0) -> int:
     return load_library().hqq_dequantize(packed_codes, scale_f16, zero_f16, rows, cols, nbits,
                                          group_size, W_out_f16, stream)
+
+
+def hqq_matmul_backward(dY_f16: int, M: int, N: int, packed_codes: int, scale_f16: int,
+                        zero_f16: int, K: int, nbits: int, group_size: int, dX: int, out_f32: int,
+                        workspace: int = 0, stream: int = 0) -> int:
+    return load_library().hqq_matmul_backward(dY_f16, M, N, packed_codes, scale_f16, zero_f16, K,
+                                              nbits, group_size, dX, out_f32, workspace, stream)
+
+
+def hqq_matmul_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return load_library().hqq_matmul_backward_workspace_bytes(M, N, K)
+
+
+def hqq_expert_sort(ids_i32: int, tokens: int, topk: int, experts: int, order_i32: int,
+                    position_i32: int, offsets_i32: int, workspace: int = 0,
+                    stream: int = 0) -> int:
+    return load_library().hqq_expert_sort(ids_i32, tokens, topk, experts, order_i32, position_i32,
+                                          offsets_i32, workspace, stream)
+
+
+def hqq_expert_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
+    return load_library().hqq_expert_sort_workspace_bytes(tokens, topk, experts)
+
+
+def hqq_expert_gather(X: int, dtype: int, tokens: int, topk: int, width: int, position_i32: int,
+                      Xs: int, stream: int = 0) -> int:
+    return load_library().hqq_expert_gather(X, dtype, tokens, topk, width, position_i32, Xs, stream)
+
+
+def hqq_expert_combine(Ys: int, dtype: int, tokens: int, topk: int, width: int, position_i32: int,
+                       weights_f32: int, out: int, stream: int = 0) -> int:
+    return load_library().hqq_expert_combine(Ys, dtype, tokens, topk, width, position_i32,
+                                             weights_f32, out, stream)
+
+
+def hqq_expert_combine_backward(dOut: int, Ys: int, dtype: int, tokens: int, topk: int, width: int,
+                                position_i32: int, weights_f32: int, dYs: int, dweights_f32: int,
+                                stream: int = 0) -> int:
+    return load_library().hqq_expert_combine_backward(dOut, Ys, dtype, tokens, topk, width,
+                                                      position_i32, weights_f32, dYs, dweights_f32,
+                                                      stream)
+
+
+def hqq_matmul_experts(X_f16: int, rows: int, K: int, order_i32: int, topk: int, offsets_i32: int,
+                       experts: int, packed_codes: int, scale_f16: int, zero_f16: int, N: int,
+                       nbits: int, group_size: int, Y: int, out_f32: int, stream: int = 0) -> int:
+    return load_library().hqq_matmul_experts(X_f16, rows, K, order_i32, topk, offsets_i32, experts,
+                                             packed_codes, scale_f16, zero_f16, N, nbits,
+                                             group_size, Y, out_f32, stream)
+
+
+def hqq_matmul_experts_backward(dY_f16: int, rows: int, N: int, offsets_i32: int, experts: int,
+                                packed_codes: int, scale_f16: int, zero_f16: int, K: int,
+                                nbits: int, group_size: int, dX: int, out_f32: int,
+                                workspace: int = 0, stream: int = 0) -> int:
+    return load_library().hqq_matmul_experts_backward(dY_f16, rows, N, offsets_i32, experts,
+                                                      packed_codes, scale_f16, zero_f16, K, nbits,
+                                                      group_size, dX, out_f32, workspace, stream)
+
+
+def hqq_matmul_experts_backward_workspace_bytes(rows: int, N: int, K: int, experts: int) -> int:
+    return load_library().hqq_matmul_experts_backward_workspace_bytes(rows, N, K, experts)
+
+
+def hqq_adapters(X: int, dtype: int, M: int, K: int, A: int, B: int, N: int, rank: int,
+                 adapters: int, ids_i32: int, scales_f32: int, base: int, base_f32: int, Y: int,
+                 out_f32: int, workspace: int, stream: int = 0) -> int:
+    return load_library().hqq_adapters(X, dtype, M, K, A, B, N, rank, adapters, ids_i32, scales_f32,
+                                       base, base_f32, Y, out_f32, workspace, stream)
+
+
+def hqq_adapters_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
+    return load_library().hqq_adapters_workspace_bytes(M, N, K, rank, adapters)
+
+
+def hqq_adapters_backward(dY: int, X: int, dtype: int, M: int, K: int, A: int, B: int, N: int,
+                          rank: int, adapters: int, ids_i32: int, scales_f32: int, base: int,
+                          base_f32: int, dX: int, out_f32: int, dA_f32: int, dB_f32: int,
+                          workspace: int, stream: int = 0) -> int:
+    return load_library().hqq_adapters_backward(dY, X, dtype, M, K, A, B, N, rank, adapters, ids_i32,
+                                                scales_f32, base, base_f32, dX, out_f32, dA_f32,
+                                                dB_f32, workspace, stream)
+
+
+def hqq_adapters_backward_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
+    return load_library().hqq_adapters_backward_workspace_bytes(M, N, K, rank, adapters)
 
 
 # ----------------------------------------------------------- torch helpers --
@@ -675,3 +792,337 @@ def dequantize(q: QuantizedWeight, out=None, stream=None):
     if st != HQQ_OK:
         raise HQQError(st, "hqq_dequantize")
     return out
+
+
+# ----------------------------------------- experts, adapters, their gradients --
+
+@dataclass
+class ExpertOrder:
+    """The (token, choice) slots of a routed layer sorted by expert (:func:`expert_sort`)."""
+    order: "torch.Tensor"             # int32, tokens * topk: slot of a sorted row (~slot: dropped)
+    position: "torch.Tensor"          # int32, tokens * topk: sorted row of a slot (~row: dropped)
+    offsets: "torch.Tensor"           # int32, experts + 1: first sorted row of an expert
+    tokens: int
+    topk: int
+    experts: int
+
+    @property
+    def rows(self) -> int:
+        return self.tokens * self.topk
+
+
+def _launch(device, stream, call):
+    """``call(stream handle)`` with ``device`` current and allocations tied to the stream."""
+    import torch
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        with torch.cuda.stream(stream):
+            return call(int(stream.cuda_stream))
+    if device.index == torch.cuda.current_device():
+        return call(int(torch.cuda.current_stream().cuda_stream))
+    with torch.cuda.device(device):
+        return call(int(torch.cuda.current_stream().cuda_stream))
+
+
+def _take(t, name: str, dtype, shape, device):
+    """Checks a tensor argument: its type (one, or one of a tuple), shape and device."""
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _check_status(st: int, where: str) -> None:
+    if st != HQQ_OK:
+        raise HQQError(st, where)
+
+
+def _need(nbytes: int, where: str) -> int:
+    if nbytes < 0:
+        raise HQQError(HQQ_ERR_INVALID_ARG, where)
+    return nbytes
+
+
+def _scratch(workspace, nbytes: int, device):
+    """The caller's workspace if it is large enough, or a new one; None where none is needed."""
+    import torch
+    if nbytes == 0:
+        return None
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or \
+            workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace needs {nbytes} bytes of memory of {device}")
+    return workspace
+
+
+def _result(out, shape, dtype, device):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _take(out, "out", dtype, shape, device)
+
+
+def _element(t, name: str) -> int:
+    import torch
+    code = {torch.float16: HQQ_DTYPE_F16, torch.bfloat16: HQQ_DTYPE_BF16,
+            torch.float32: HQQ_DTYPE_F32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, not {t.dtype}")
+    return code
+
+
+def _weight_on(q: "QuantizedWeight", device) -> None:
+    if q.packed.device != device or q.scale.device != device or q.zero.device != device:
+        raise ValueError(f"the weight is on {q.packed.device}, the rows are on {device}")
+
+
+def expert_sort(ids, experts: int, workspace=None, stream=None) -> ExpertOrder:
+    """Stable order of the (token, choice) slots by expert (hqq_expert_sort).  ``ids`` is a
+    tokens x topk (or flat: topk 1) int32 CUDA tensor; values outside [0, experts) drop the slot."""
+    import torch
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids must be tokens x topk, or flat")
+    dev = _take(ids, "ids", torch.int32, None, None).device
+    tokens, topk = ids.shape[0], (ids.shape[1] if ids.dim() == 2 else 1)
+    wb = _need(hqq_expert_sort_workspace_bytes(tokens, topk, experts), "hqq_expert_sort")
+
+    def call(sh):
+        ws = _scratch(workspace, wb, dev)
+        n = tokens * topk
+        order, position, offsets = torch.empty(2 * n + experts + 1, dtype=torch.int32,
+                                               device=dev).split((n, n, experts + 1))
+        _check_status(hqq_expert_sort(_addr(ids), tokens, topk, experts, _addr(order),
+                                      _addr(position), _addr(offsets), _addr(ws), sh),
+                      "hqq_expert_sort")
+        return ExpertOrder(order, position, offsets, tokens, topk, experts)
+    return _launch(dev, stream, call)
+
+
+def expert_gather(X, route: ExpertOrder, out=None, stream=None):
+    """The tokens' rows in sorted order, zeros for dropped slots (hqq_expert_gather).  The
+    gradient is ``expert_combine(dXs, route)``."""
+    code = _element(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be tokens x width")
+    dev, width = route.order.device, X.shape[1]
+    _take(X, "X", X.dtype, (route.tokens, width), dev)
+
+    def call(sh):
+        y = _result(out, (route.rows, width), X.dtype, dev)
+        _check_status(hqq_expert_gather(_addr(X), code, route.tokens, route.topk, width,
+                                        _addr(route.position), _addr(y), sh), "hqq_expert_gather")
+        return y
+    return _launch(dev, stream, call)
+
+
+def _weights_of(weights, route: ExpertOrder):
+    import torch
+    if weights is None:
+        return None
+    if weights.numel() != route.rows:
+        raise ValueError(f"weights has {weights.numel()} elements, expected {route.rows}")
+    return _take(weights, "weights", torch.float32, None, route.order.device)
+
+
+def expert_combine(Ys, route: ExpertOrder, weights=None, out=None, stream=None):
+    """Every token's weighted sum of its kept sorted rows (hqq_expert_combine).  ``weights`` is a
+    tokens x topk float32 CUDA tensor, or None (weights of 1)."""
+    code = _element(Ys, "Ys")
+    if Ys.dim() != 2:
+        raise ValueError("Ys must be rows x width")
+    dev, width = route.order.device, Ys.shape[1]
+    _take(Ys, "Ys", Ys.dtype, (route.rows, width), dev)
+    w = _weights_of(weights, route)
+
+    def call(sh):
+        y = _result(out, (route.tokens, width), Ys.dtype, dev)
+        _check_status(hqq_expert_combine(_addr(Ys), code, route.tokens, route.topk, width,
+                                         _addr(route.position), _addr(w), _addr(y), sh),
+                      "hqq_expert_combine")
+        return y
+    return _launch(dev, stream, call)
+
+
+def expert_combine_backward(dOut, Ys, route: ExpertOrder, weights=None, stream=None):
+    """The gradients of :func:`expert_combine`: (dYs, dweights) (hqq_expert_combine_backward).
+    Without ``weights`` only dYs (dweights is None), and ``Ys`` may be None."""
+    import torch
+    code = _element(dOut, "dOut")
+    if dOut.dim() != 2:
+        raise ValueError("dOut must be tokens x width")
+    dev, width = route.order.device, dOut.shape[1]
+    _take(dOut, "dOut", dOut.dtype, (route.tokens, width), dev)
+    w = _weights_of(weights, route)
+    if w is not None or Ys is not None:
+        _take(Ys, "Ys", dOut.dtype, (route.rows, width), dev)
+
+    def call(sh):
+        dYs = torch.empty((route.rows, width), dtype=dOut.dtype, device=dev)
+        dw = None if w is None else torch.empty((route.tokens, route.topk), dtype=torch.float32,
+                                                device=dev)
+        _check_status(hqq_expert_combine_backward(
+            _addr(dOut), _addr(Ys), code, route.tokens, route.topk, width, _addr(route.position),
+            _addr(w), _addr(dYs), _addr(dw), sh), "hqq_expert_combine_backward")
+        return dYs, dw
+    return _launch(dev, stream, call)
+
+
+def _expert_rows(q: "QuantizedWeight", route: ExpertOrder) -> int:
+    if q.rows % route.experts != 0:
+        raise ValueError(f"{q.rows} weight rows are not {route.experts} experts of equal size")
+    return q.rows // route.experts
+
+
+def matmul_experts(X, q: "QuantizedWeight", route: ExpertOrder, sorted_rows: bool = False,
+                   out_f32: bool = False, out=None, stream=None):
+    """The products of the sorted rows with their experts' quantized weights
+    (hqq_matmul_experts): rows x N float16 (or float32).  ``q`` holds the experts' N x K weights
+    below each other.  ``X`` holds the tokens' rows (float16), or with ``sorted_rows`` the sorted
+    rows themselves."""
+    import torch
+    dev, K, N = route.order.device, q.cols, _expert_rows(q, route)
+    _take(X, "X", torch.float16, (route.rows if sorted_rows else route.tokens, K), dev)
+    _weight_on(q, dev)
+
+    def call(sh):
+        y = _result(out, (route.rows, N), torch.float32 if out_f32 else torch.float16, dev)
+        _check_status(hqq_matmul_experts(
+            _addr(X), route.rows, K, 0 if sorted_rows else _addr(route.order), route.topk,
+            _addr(route.offsets), route.experts, _addr(q.packed), _addr(q.scale), _addr(q.zero), N,
+            q.nbits, q.group_size, _addr(y), int(bool(out_f32)), sh), "hqq_matmul_experts")
+        return y
+    return _launch(dev, stream, call)
+
+
+def matmul_experts_backward(dYs, q: "QuantizedWeight", route: ExpertOrder, out_f32: bool = False,
+                            out=None, workspace=None, stream=None):
+    """The gradient of the sorted rows, dX = dY Q^-1(W_e) (hqq_matmul_experts_backward), rows x K
+    float16 (or float32).  ``expert_combine`` of it without weights is the tokens' gradient."""
+    import torch
+    dev, K, N = route.order.device, q.cols, _expert_rows(q, route)
+    _take(dYs, "dYs", torch.float16, (route.rows, N), dev)
+    _weight_on(q, dev)
+    wb = _need(hqq_matmul_experts_backward_workspace_bytes(route.rows, N, K, route.experts),
+               "hqq_matmul_experts_backward")
+
+    def call(sh):
+        y = _result(out, (route.rows, K), torch.float32 if out_f32 else torch.float16, dev)
+        ws = _scratch(workspace, wb, dev)
+        _check_status(hqq_matmul_experts_backward(
+            _addr(dYs), route.rows, N, _addr(route.offsets), route.experts, _addr(q.packed),
+            _addr(q.scale), _addr(q.zero), K, q.nbits, q.group_size, _addr(y), int(bool(out_f32)),
+            _addr(ws), sh), "hqq_matmul_experts_backward")
+        return y
+    return _launch(dev, stream, call)
+
+
+def matmul_backward(dY, q: "QuantizedWeight", out_f32: bool = False, out=None, workspace=None,
+                    stream=None):
+    """The gradient of :func:`matmul`'s activations, dX = dY Q^-1(W_q) (hqq_matmul_backward): an
+    M x K float16 (or float32) tensor for a contiguous M x N float16 CUDA tensor dY."""
+    import torch
+    if dY.dim() != 2:
+        raise ValueError("dY must be M x N")
+    M, dev = dY.shape[0], dY.device
+    _take(dY, "dY", torch.float16, (M, q.rows), dev)
+    _weight_on(q, dev)
+    wb = _need(hqq_matmul_backward_workspace_bytes(M, q.rows, q.cols), "hqq_matmul_backward")
+
+    def call(sh):
+        y = _result(out, (M, q.cols), torch.float32 if out_f32 else torch.float16, dev)
+        ws = _scratch(workspace, wb, dev)
+        _check_status(hqq_matmul_backward(
+            _addr(dY), M, q.rows, _addr(q.packed), _addr(q.scale), _addr(q.zero), q.cols, q.nbits,
+            q.group_size, _addr(y), int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_backward")
+        return y
+    return _launch(dev, stream, call)
+
+
+def _adapter_shapes(X, A, B, ids, scales):
+    """Checks the tensors of an adapter call; returns (dtype code, M, K, N, rank, adapters)."""
+    import torch
+    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("X must be M x K, A adapters x rank x K, B adapters x N x rank")
+    (M, K), (n, rank), N, dev = X.shape, A.shape[:2], B.shape[1], X.device
+    _take(X, "X", (torch.float16, torch.bfloat16), None, dev)
+    _take(A, "A", X.dtype, (n, rank, K), dev)
+    _take(B, "B", X.dtype, (n, N, rank), dev)
+    _take(ids, "ids", torch.int32, (M,), dev)
+    _take(scales, "scales", torch.float32, (n,), dev)
+    return _element(X, "X"), M, K, N, rank, n
+
+
+def _base_f32(base, X, shape) -> int:
+    import torch
+    if base is None:
+        return 0
+    _take(base, "base", (X.dtype, torch.float32), shape, X.device)
+    return int(base.dtype == torch.float32)
+
+
+def adapters(X, A, B, ids, scales, base=None, out_f32: bool = False, out=None, workspace=None,
+             stream=None):
+    """Low-rank adapters of many requests (hqq_adapters): base[m] + scales[a] B[a] (A[a] X[m]) with
+    a = ids[m], or base[m] where ids[m] names no adapter.  X: M x K float16 or bfloat16; A:
+    adapters x rank x K, B: adapters x N x rank of X's type; ids: M int32; scales: adapters
+    float32; base: M x N of X's type or float32, or None (zeros).  Returns M x N of X's type (or
+    float32); ``out`` may be ``base``."""
+    import torch
+    code, M, K, N, rank, n = _adapter_shapes(X, A, B, ids, scales)
+    dev, b32 = X.device, _base_f32(base, X, (M, N))
+    wb = _need(hqq_adapters_workspace_bytes(M, N, K, rank, n), "hqq_adapters")
+
+    def call(sh):
+        y = _result(out, (M, N), torch.float32 if out_f32 else X.dtype, dev)
+        ws = _scratch(workspace, wb, dev)
+        _check_status(hqq_adapters(
+            _addr(X), code, M, K, _addr(A), _addr(B), N, rank, n, _addr(ids), _addr(scales),
+            _addr(base), b32, _addr(y), int(bool(out_f32)), _addr(ws), sh), "hqq_adapters")
+        return y
+    return _launch(dev, stream, call)
+
+
+def adapters_backward(dY, X, A, B, ids, scales, base=None, out_f32: bool = False, out=None,
+                      workspace=None, stream=None):
+    """The gradients of :func:`adapters` (hqq_adapters_backward): (dX, dA, dB), dX of X's type (or
+    float32) with ``base`` (M x K) added, dA and dB float32."""
+    import torch
+    code, M, K, N, rank, n = _adapter_shapes(X, A, B, ids, scales)
+    dev, b32 = X.device, _base_f32(base, X, (M, K))
+    _take(dY, "dY", X.dtype, (M, N), dev)
+    wb = _need(hqq_adapters_backward_workspace_bytes(M, N, K, rank, n), "hqq_adapters_backward")
+
+    def call(sh):
+        dX = _result(out, (M, K), torch.float32 if out_f32 else X.dtype, dev)
+        dA = torch.empty((n, rank, K), dtype=torch.float32, device=dev)
+        dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, wb, dev)
+        _check_status(hqq_adapters_backward(
+            _addr(dY), _addr(X), code, M, K, _addr(A), _addr(B), N, rank, n, _addr(ids),
+            _addr(scales), _addr(base), b32, _addr(dX), int(bool(out_f32)), _addr(dA), _addr(dB),
+            _addr(ws), sh), "hqq_adapters_backward")
+        return dX, dA, dB
+    return _launch(dev, stream, call)
+
+
+def matmul_adapters(X, q: "QuantizedWeight", A, B, ids, scales, out_f32: bool = False, out=None,
+                    stream=None):
+    """X Q^-1(W_q)^T plus every row's adapter: :func:`matmul` in float32, then :func:`adapters`
+    (float16 X; the sum is rounded once)."""
+    base = matmul(X, q, out_f32=True, stream=stream)
+    return adapters(X, A, B, ids, scales, base=base, out_f32=out_f32, out=out, stream=stream)
+
+
+def matmul_adapters_backward(dY, X, q: "QuantizedWeight", A, B, ids, scales, out_f32: bool = False,
+                             out=None, stream=None):
+    """The gradients of :func:`matmul_adapters` for a frozen weight: (dX, dA, dB)."""
+    base = matmul_backward(dY, q, out_f32=True, stream=stream)
+    return adapters_backward(dY, X, A, B, ids, scales, base=base, out_f32=out_f32, out=out,
+                             stream=stream)

@@ -10,9 +10,12 @@
 #include <mutex>
 
 #include "../../include/hqq.h"
+#include "hqq_adapters.h"
 #include "hqq_internal.h"
 #include "hqq_lowrank.h"
 #include "hqq_matmul.h"
+#include "hqq_matmul_t.h"
+#include "hqq_route.h"
 #include "hqq_tensor_stop.h"
 
 namespace {
@@ -586,6 +589,329 @@ int hqq_meta_dequantize(const void* codes_u8, const void* mscale_f16, const void
       static_cast<const uint16_t*>(moffset_f16), n, meta_group, static_cast<uint16_t*>(values_f16),
       cus, static_cast<hipStream_t>(stream));
   return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- experts and adapters --
+
+namespace {
+
+constexpr int64_t kMaxGroupedRows = 8000000;  // row tiles of the grid's second dimension
+constexpr int64_t kMaxAdapterRows = 4000000;
+
+int group_shift_of(int group_size) {
+  return group_size == 16 ? 4 : group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+}
+
+// Shapes, widths and the weight's pointers of a product with experts (0: one) N x K weights.
+int validate_product(int64_t M, int64_t N, int64_t K, int experts, int nbits, int group_size) {
+  const int64_t n = experts > 0 ? checked_elems(experts, N) : N;
+  if (n < 0 || checked_elems(M, K) < 0 || checked_elems(n, K) < 0 || checked_elems(M, N) < 0)
+    return HQQ_ERR_INVALID_ARG;
+  if (!supported_nbits(nbits) || !supported_group(group_size)) return HQQ_ERR_UNSUPPORTED;
+  if (K % group_size != 0) return HQQ_ERR_INVALID_ARG;
+  if (K % 32 != 0) return HQQ_ERR_UNSUPPORTED;
+  return M > kMaxGroupedRows ? HQQ_ERR_INVALID_ARG : HQQ_OK;
+}
+
+int validate_experts(int experts) {
+  if (experts < 1) return HQQ_ERR_INVALID_ARG;
+  return experts > hqq::kMaxExperts ? HQQ_ERR_UNSUPPORTED : HQQ_OK;
+}
+
+// dX = dY Q^-1(W_q) for one weight (offsets null, experts 0) or sorted rows.
+int matmul_backward(const void* dY, int64_t M, int64_t N, const void* offsets, int experts,
+                    const void* packed, const void* scale, const void* zero, int64_t K, int nbits,
+                    int group_size, void* dX, int out_f32, void* workspace, void* stream) {
+  const int st = validate_product(M, N, K, experts, nbits, group_size);
+  if (st != HQQ_OK) return st;
+  if (out_f32 != 0 && out_f32 != 1) return HQQ_ERR_INVALID_ARG;
+  if (M == 0 || K == 0) return HQQ_OK;
+  if (!dX || (experts > 0 && !offsets)) return HQQ_ERR_INVALID_ARG;
+  if (N > 0 && (!dY || !packed || !scale || !zero)) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(dX, out_f32 ? 4 : 2) || !aligned(offsets, 4)) return HQQ_ERR_ALIGNMENT;
+  if (N > 0 && (!aligned(dY, 2) || !aligned(packed, 16) || !aligned(scale, 2) || !aligned(zero, 2)))
+    return HQQ_ERR_ALIGNMENT;
+  if (hqq::matmul_t_workspace_bytes(M, N, K, experts) > 0) {
+    if (!workspace) return HQQ_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return HQQ_ERR_ALIGNMENT;
+  }
+  hqq::MatmulTParams p;
+  p.dY = static_cast<const uint16_t*>(dY);
+  p.packed = static_cast<const uint8_t*>(packed);
+  p.scale16 = static_cast<const uint16_t*>(scale);
+  p.zero16 = static_cast<const uint16_t*>(zero);
+  p.dX = dX;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.nbits = nbits;
+  p.group_size = group_size;
+  p.group_shift = group_shift_of(group_size);
+  p.out_f32 = out_f32;
+  p.offsets = static_cast<const int32_t*>(offsets);
+  p.experts = experts;
+  p.part = static_cast<float*>(workspace);
+  p.nsplit = 1;
+  return hqq::launch_matmul_t(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int64_t slots_of(int64_t tokens, int topk) {
+  if (tokens < 0 || topk < 1 || tokens > (int64_t)INT32_MAX / topk) return -1;
+  return tokens * topk;
+}
+
+int64_t dtype_bytes(int dtype) { return dtype == HQQ_DTYPE_F32 ? 4 : 2; }
+
+// Sizes and pointers that the row entry points share.
+int validate_rows(int dtype, int64_t tokens, int topk, int64_t width) {
+  const int64_t slots = slots_of(tokens, topk);
+  if (slots < 0 || checked_elems(slots, width) < 0) return HQQ_ERR_INVALID_ARG;
+  if (dtype != HQQ_DTYPE_F16 && dtype != HQQ_DTYPE_BF16 && dtype != HQQ_DTYPE_F32)
+    return HQQ_ERR_UNSUPPORTED;
+  return HQQ_OK;
+}
+
+int validate_adapters(int dtype, int64_t M, int64_t N, int64_t K, int rank, int adapters) {
+  if (M < 0 || N < 1 || K < 1 || rank < 1 || adapters < 1 || M > kMaxAdapterRows) return HQQ_ERR_INVALID_ARG;
+  if (dtype != HQQ_DTYPE_F16 && dtype != HQQ_DTYPE_BF16) return HQQ_ERR_UNSUPPORTED;
+  if (rank % 8 != 0 || rank > hqq::kMaxAdapterRank || adapters > hqq::kMaxAdapters || K % 8 != 0)
+    return HQQ_ERR_UNSUPPORTED;
+  const int64_t factors = (int64_t)rank * adapters;  // at most 2^18
+  if (N > INT64_MAX / 64 - 8 || checked_elems(M, K) < 0 || checked_elems(M, N) < 0 ||
+      checked_elems(factors, K) < 0 || checked_elems(factors, N + 7) < 0)
+    return HQQ_ERR_INVALID_ARG;
+  return HQQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hqq_matmul_backward(const void* dY_f16, int64_t M, int64_t N, const void* packed_codes,
+                        const void* scale_f16, const void* zero_f16, int64_t K, int nbits,
+                        int group_size, void* dX, int out_f32, void* workspace, void* stream) {
+  return matmul_backward(dY_f16, M, N, nullptr, 0, packed_codes, scale_f16, zero_f16, K, nbits,
+                         group_size, dX, out_f32, workspace, stream);
+}
+
+int64_t hqq_matmul_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (checked_elems(M, K) < 0 || checked_elems(N, K) < 0 || checked_elems(M, N) < 0 || M > kMaxGroupedRows)
+    return -1;
+  return M == 0 || K == 0 ? 0 : hqq::matmul_t_workspace_bytes(M, N, K, 0);
+}
+
+int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* order_i32, int topk,
+                       const void* offsets_i32, int experts, const void* packed_codes,
+                       const void* scale_f16, const void* zero_f16, int64_t N, int nbits,
+                       int group_size, void* Y, int out_f32, void* stream) {
+  int st = validate_experts(experts);
+  if (st != HQQ_OK) return st;
+  st = validate_product(rows, N, K, experts, nbits, group_size);
+  if (st != HQQ_OK) return st;
+  if ((out_f32 != 0 && out_f32 != 1) || (order_i32 && topk < 1)) return HQQ_ERR_INVALID_ARG;
+  if (rows == 0 || N == 0) return HQQ_OK;
+  if (!Y || !offsets_i32) return HQQ_ERR_INVALID_ARG;
+  if (K > 0 && (!X_f16 || !packed_codes || !scale_f16 || !zero_f16)) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(Y, out_f32 ? 4 : 2) || !aligned(offsets_i32, 4) || !aligned(order_i32, 4))
+    return HQQ_ERR_ALIGNMENT;
+  if (K > 0 && (!aligned(X_f16, 16) || !aligned(packed_codes, 16) || !aligned(scale_f16, 2) ||
+                !aligned(zero_f16, 2)))
+    return HQQ_ERR_ALIGNMENT;
+  hqq::MatmulParams p;
+  p.X = static_cast<const uint16_t*>(X_f16);
+  p.packed = static_cast<const uint8_t*>(packed_codes);
+  p.scale16 = static_cast<const uint16_t*>(scale_f16);
+  p.zero16 = static_cast<const uint16_t*>(zero_f16);
+  p.Y = Y;
+  p.M = rows;
+  p.N = N;
+  p.K = K;
+  p.nbits = nbits;
+  p.group_size = group_size;
+  p.group_shift = group_shift_of(group_size);
+  p.out_f32 = out_f32;
+  p.offsets = static_cast<const int32_t*>(offsets_i32);
+  p.order = static_cast<const int32_t*>(order_i32);
+  p.experts = experts;
+  p.topk = order_i32 ? topk : 1;
+  return hqq::launch_matmul_experts(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int hqq_matmul_experts_backward(const void* dY_f16, int64_t rows, int64_t N,
+                                const void* offsets_i32, int experts, const void* packed_codes,
+                                const void* scale_f16, const void* zero_f16, int64_t K, int nbits,
+                                int group_size, void* dX, int out_f32, void* workspace,
+                                void* stream) {
+  const int st = validate_experts(experts);
+  if (st != HQQ_OK) return st;
+  return matmul_backward(dY_f16, rows, N, offsets_i32, experts, packed_codes, scale_f16, zero_f16,
+                         K, nbits, group_size, dX, out_f32, workspace, stream);
+}
+
+int64_t hqq_matmul_experts_backward_workspace_bytes(int64_t rows, int64_t N, int64_t K,
+                                                    int experts) {
+  if (validate_experts(experts) != HQQ_OK || rows > kMaxGroupedRows) return -1;
+  const int64_t n = checked_elems(experts, N);
+  if (n < 0 || checked_elems(rows, K) < 0 || checked_elems(n, K) < 0 || checked_elems(rows, N) < 0)
+    return -1;
+  return rows == 0 || K == 0 ? 0 : hqq::matmul_t_workspace_bytes(rows, N, K, experts);
+}
+
+int64_t hqq_expert_sort_workspace_bytes(int64_t tokens, int topk, int experts) {
+  const int64_t slots = slots_of(tokens, topk);
+  if (slots < 0 || validate_experts(experts) != HQQ_OK) return -1;
+  return hqq::route_sort_workspace_bytes(slots, experts);
+}
+
+int hqq_expert_sort(const void* ids_i32, int64_t tokens, int topk, int experts, void* order_i32,
+                    void* position_i32, void* offsets_i32, void* workspace, void* stream) {
+  const int64_t slots = slots_of(tokens, topk);
+  if (slots < 0) return HQQ_ERR_INVALID_ARG;
+  const int st = validate_experts(experts);
+  if (st != HQQ_OK) return st;
+  if (!offsets_i32 || (slots > 0 && (!ids_i32 || !order_i32 || !position_i32))) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(ids_i32, 4) || !aligned(order_i32, 4) || !aligned(position_i32, 4) ||
+      !aligned(offsets_i32, 4) || !aligned(workspace, 4))
+    return HQQ_ERR_ALIGNMENT;
+  if (hqq::route_sort_workspace_bytes(slots, experts) > 0 && !workspace) return HQQ_ERR_INVALID_ARG;
+  const hipError_t err = hqq::launch_route_sort(
+      static_cast<const int32_t*>(ids_i32), slots, experts, static_cast<int32_t*>(order_i32),
+      static_cast<int32_t*>(position_i32), static_cast<int32_t*>(offsets_i32),
+      static_cast<int32_t*>(workspace), static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int hqq_expert_gather(const void* X, int dtype, int64_t tokens, int topk, int64_t width,
+                      const void* position_i32, void* Xs, void* stream) {
+  const int st = validate_rows(dtype, tokens, topk, width);
+  if (st != HQQ_OK) return st;
+  if (tokens == 0 || width == 0) return HQQ_OK;
+  if (!X || !position_i32 || !Xs) return HQQ_ERR_INVALID_ARG;
+  const uintptr_t e = dtype_bytes(dtype);
+  if (!aligned(X, e) || !aligned(Xs, e) || !aligned(position_i32, 4)) return HQQ_ERR_ALIGNMENT;
+  hqq::RouteRows p = {X, nullptr, Xs, static_cast<const int32_t*>(position_i32), nullptr, nullptr, tokens, width, topk};
+  const hipError_t err = hqq::launch_route_gather(p, dtype, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int hqq_expert_combine(const void* Ys, int dtype, int64_t tokens, int topk, int64_t width,
+                       const void* position_i32, const void* weights_f32, void* out, void* stream) {
+  const int st = validate_rows(dtype, tokens, topk, width);
+  if (st != HQQ_OK) return st;
+  if (tokens == 0 || width == 0) return HQQ_OK;
+  if (!Ys || !position_i32 || !out) return HQQ_ERR_INVALID_ARG;
+  const uintptr_t e = dtype_bytes(dtype);
+  if (!aligned(Ys, e) || !aligned(out, e) || !aligned(position_i32, 4) || !aligned(weights_f32, 4))
+    return HQQ_ERR_ALIGNMENT;
+  hqq::RouteRows p = {Ys, nullptr, out, static_cast<const int32_t*>(position_i32),
+                      static_cast<const float*>(weights_f32), nullptr, tokens, width, topk};
+  const hipError_t err = hqq::launch_route_combine(p, dtype, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int hqq_expert_combine_backward(const void* dOut, const void* Ys, int dtype, int64_t tokens,
+                                int topk, int64_t width, const void* position_i32,
+                                const void* weights_f32, void* dYs, void* dweights_f32,
+                                void* stream) {
+  const int st = validate_rows(dtype, tokens, topk, width);
+  if (st != HQQ_OK) return st;
+  if (tokens == 0 || (width == 0 && !dweights_f32)) return HQQ_OK;
+  if (!position_i32 || (width > 0 && (!dOut || !dYs || (dweights_f32 && !Ys)))) return HQQ_ERR_INVALID_ARG;
+  const uintptr_t e = dtype_bytes(dtype);
+  if (!aligned(dOut, e) || !aligned(Ys, e) || !aligned(dYs, e) || !aligned(position_i32, 4) ||
+      !aligned(weights_f32, 4) || !aligned(dweights_f32, 4))
+    return HQQ_ERR_ALIGNMENT;
+  hqq::RouteRows p = {Ys, dOut, dYs, static_cast<const int32_t*>(position_i32),
+                      static_cast<const float*>(weights_f32), static_cast<float*>(dweights_f32),
+                      tokens, width, topk};
+  const hipError_t err = hqq::launch_route_combine_backward(p, dtype, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int64_t hqq_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters) {
+  if (validate_adapters(HQQ_DTYPE_F16, M, N, K, rank, adapters) != HQQ_OK) return -1;
+  return hqq::adapters_workspace_bytes(M, N, K, rank, adapters);
+}
+
+int64_t hqq_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank,
+                                              int adapters) {
+  if (validate_adapters(HQQ_DTYPE_F16, M, N, K, rank, adapters) != HQQ_OK) return -1;
+  return hqq::adapters_backward_workspace_bytes(M, N, K, rank, adapters);
+}
+
+int hqq_adapters(const void* X, int dtype, int64_t M, int64_t K, const void* A, const void* B,
+                 int64_t N, int rank, int adapters, const void* ids_i32, const void* scales_f32,
+                 const void* base, int base_f32, void* Y, int out_f32, void* workspace,
+                 void* stream) {
+  const int st = validate_adapters(dtype, M, N, K, rank, adapters);
+  if (st != HQQ_OK) return st;
+  if ((base_f32 != 0 && base_f32 != 1) || (out_f32 != 0 && out_f32 != 1)) return HQQ_ERR_INVALID_ARG;
+  if (M == 0) return HQQ_OK;
+  if (!X || !A || !B || !ids_i32 || !scales_f32 || !Y || !workspace) return HQQ_ERR_INVALID_ARG;
+  if (base == Y && base_f32 != out_f32) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(ids_i32, 4) ||
+      !aligned(scales_f32, 4) || !aligned(base, base_f32 ? 4 : 2) || !aligned(Y, out_f32 ? 4 : 2) ||
+      !aligned(workspace, 256))
+    return HQQ_ERR_ALIGNMENT;
+  hqq::AdapterParams p = {};
+  p.dtype = dtype;
+  p.X = static_cast<const uint16_t*>(X);
+  p.A = static_cast<const uint16_t*>(A);
+  p.B = static_cast<const uint16_t*>(B);
+  p.ids = static_cast<const int32_t*>(ids_i32);
+  p.scales = static_cast<const float*>(scales_f32);
+  p.base = base;
+  p.base_f32 = base_f32;
+  p.out = Y;
+  p.out_f32 = out_f32;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.rank = rank;
+  p.adapters = adapters;
+  p.workspace = workspace;
+  return hqq::launch_adapters(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int hqq_adapters_backward(const void* dY, const void* X, int dtype, int64_t M, int64_t K,
+                          const void* A, const void* B, int64_t N, int rank, int adapters,
+                          const void* ids_i32, const void* scales_f32, const void* base,
+                          int base_f32, void* dX, int out_f32, void* dA_f32, void* dB_f32,
+                          void* workspace, void* stream) {
+  const int st = validate_adapters(dtype, M, N, K, rank, adapters);
+  if (st != HQQ_OK) return st;
+  if ((base_f32 != 0 && base_f32 != 1) || (out_f32 != 0 && out_f32 != 1)) return HQQ_ERR_INVALID_ARG;
+  if (!dA_f32 || !dB_f32 || !workspace) return HQQ_ERR_INVALID_ARG;
+  if (M > 0 && (!dY || !X || !A || !B || !ids_i32 || !scales_f32 || !dX)) return HQQ_ERR_INVALID_ARG;
+  if (base && base == dX && base_f32 != out_f32) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(dY, 2) || !aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) ||
+      !aligned(ids_i32, 4) || !aligned(scales_f32, 4) || !aligned(base, base_f32 ? 4 : 2) ||
+      !aligned(dX, out_f32 ? 4 : 2) || !aligned(dA_f32, 16) || !aligned(dB_f32, 16) ||
+      !aligned(workspace, 256))
+    return HQQ_ERR_ALIGNMENT;
+  hqq::AdapterParams p = {};
+  p.dtype = dtype;
+  p.X = static_cast<const uint16_t*>(X);
+  p.A = static_cast<const uint16_t*>(A);
+  p.B = static_cast<const uint16_t*>(B);
+  p.ids = static_cast<const int32_t*>(ids_i32);
+  p.scales = static_cast<const float*>(scales_f32);
+  p.base = base;
+  p.base_f32 = base_f32;
+  p.out = dX;
+  p.out_f32 = out_f32;
+  p.dY = static_cast<const uint16_t*>(dY);
+  p.dA = static_cast<float*>(dA_f32);
+  p.dB = static_cast<float*>(dB_f32);
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.rank = rank;
+  p.adapters = adapters;
+  p.workspace = workspace;
+  return hqq::launch_adapters_backward(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
 }
 
 }  // extern "C"

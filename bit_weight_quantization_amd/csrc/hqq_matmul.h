@@ -19,6 +19,10 @@ struct MatmulParams {
   float* part;              // split-K partial slabs (caller's workspace), or null
   int64_t slab;             // floats per partial slab: M*N rounded up to a multiple of 4
   int ksplit;               // splits of K (1: no partials)
+  // products of many experts (GROUPED kernels): M rows sorted by expert, experts x N x K codes
+  const int32_t* offsets = nullptr;  // first row of every expert, experts + 1 values
+  const int32_t* order = nullptr;    // null: X holds the sorted rows; else row i is X[order[i] / topk]
+  int experts = 0, topk = 1;
 };
 
 // Rows of X up to which the wavefront-per-row kernel is used (kGemvAlignedMaxRows where
@@ -29,6 +33,8 @@ constexpr int kGemvMaxRows = 8;
 constexpr int kGemvAlignedMaxRows = 2;
 constexpr int kSkinnyMaxRows = 64;
 constexpr int kSplitMinRows = 16;  // above this (and up to kSkinnyMaxRows) K is split
+// Sorted rows of many experts up to which every row is a product of its own.
+constexpr int kExpertGemvMaxRows = 8;
 
 // Bytes of workspace the product needs for these shapes (the split-K partial slabs of
 // the skinny path; 0 when the path writes Y directly).  Depends on the shapes only.
@@ -36,5 +42,8 @@ int64_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits, int g
 
 // `prm.part` must hold matmul_workspace_bytes(...) bytes where that is not 0.
 hipError_t launch_matmul(MatmulParams prm, int cus, hipStream_t stream);
+
+// The products of sorted rows with their experts' weights: prm.offsets set.
+hipError_t launch_matmul_experts(MatmulParams prm, hipStream_t stream);
 
 }  // namespace hqq

@@ -1,0 +1,91 @@
+// hqq_tiles.h -- tiles of rows sorted into groups (experts or adapters), found on the device
+// from the groups' row offsets, so that no count has to come back to the host.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "hqq_internal.h"
+
+namespace hqq {
+
+// Upper bound of the tiles of `tile_rows` rows that `rows` rows in `groups` groups (and the
+// rows of no group) can have: every group adds at most one tile that is not full.
+inline int64_t max_row_tiles(int64_t rows, int64_t groups, int64_t tile_rows) {
+  return rows / tile_rows + (groups + 1 < rows ? groups + 1 : rows);
+}
+
+struct RowTile {
+  int group;       // in [0, groups], or -1: no such tile.  `groups`: rows of no group
+  int64_t row0;    // first sorted row
+  int rows;        // rows of the tile, 0 where there is none
+  int index;       // index of the tile within its group
+  int64_t group0;  // first sorted row of its group
+  int64_t group_rows;
+};
+
+// Tile number `tile` of `tile_rows` rows, groups in order, the rows behind the last group
+// last.  The whole wavefront calls it with equal arguments; a lane counts one group's tiles.
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* offsets, int groups, int64_t rows,
+                                                 int tile_rows, int64_t tile) {
+  const int lane = threadIdx.x & (kWave - 1);
+  RowTile t = {-1, 0, 0, 0, 0, 0};
+  int64_t before = 0;
+  for (int g0 = 0; g0 <= groups; g0 += kWave) {
+    const int g = g0 + lane;
+    int start = 0, count = 0;
+    if (g <= groups) {
+      const int last = (int)rows;
+      start = min(max(offsets[g], 0), last);  // (never outside the rows, whatever is stored)
+      count = max((g < groups ? min(offsets[g + 1], last) : last) - start, 0);
+    }
+    const int tiles = (count + tile_rows - 1) / tile_rows;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(upto, o, kWave);
+      if (lane >= o) upto += v;
+    }
+    const uint64_t hit = __ballot(before + upto > tile);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const int first = __builtin_amdgcn_readlane(upto - tiles, l);
+      t.group = g0 + l;
+      t.index = (int)(tile - before) - first;
+      t.group0 = __builtin_amdgcn_readlane(start, l);
+      t.group_rows = __builtin_amdgcn_readlane(count, l);
+      t.row0 = t.group0 + (int64_t)t.index * tile_rows;
+      const int64_t left = t.group_rows - (int64_t)t.index * tile_rows;
+      t.rows = (int)(left < tile_rows ? left : tile_rows);
+      return t;
+    }
+    before += __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+  return t;
+}
+
+// The tiles of group `group`: number of its first tile, and how many.  As find_row_tile.
+struct GroupTiles {
+  int64_t first;
+  int count;
+};
+__device__ __forceinline__ GroupTiles find_group_tiles(const int32_t* offsets, int64_t rows,
+                                                       int tile_rows, int group) {
+  const int lane = threadIdx.x & (kWave - 1), last = (int)rows;
+  GroupTiles t = {0, 0};
+  for (int g0 = 0; g0 <= group; g0 += kWave) {
+    const int g = g0 + lane;
+    int tiles = 0;
+    if (g <= group) {
+      const int start = min(max(offsets[g], 0), last);
+      tiles = (max(min(offsets[g + 1], last) - start, 0) + tile_rows - 1) / tile_rows;
+    }
+    if (group < g0 + kWave) t.count = __builtin_amdgcn_readlane(tiles, group - g0);
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) tiles += __shfl_xor(tiles, o, kWave);
+    t.first += tiles;
+  }
+  t.first -= t.count;
+  return t;
+}
+
+}  // namespace hqq

@@ -417,6 +417,189 @@ int hqq_lowrank(const void* W_f16, const void* packed_codes, const void* scale_f
 /* Bytes of the workspace of hqq_lowrank; -1 for invalid shapes or widths. */
 int64_t hqq_lowrank_workspace_bytes(int64_t rows, int64_t cols, int rank, int oversample);
 
+/*
+ * hqq_matmul_backward -- the gradient of hqq_matmul's activations: dX = dY Q^-1(W_q), for a
+ * frozen weight,
+ *   dX[m][k] = sum over n of dY[m][n] * s[n][k/g] * (q[n][k] - z[n][k/g]).
+ * The weight is dequantized to binary16 (s*q - s*z in fp32, one rounding, then to binary16)
+ * and multiplied on the matrix cores with fp32 accumulation, in an order fixed by the shapes.
+ *
+ * dY_f16       M x N binary16, row-major, 2-byte aligned.
+ * M, N, K      >= 0; K a multiple of group_size and of 32 (else HQQ_ERR_UNSUPPORTED);
+ *              M <= 8000000.  M == 0 or K == 0 is a no-op; N == 0 writes zeros.
+ * packed_codes, scale_f16, zero_f16, nbits, group_size  the N x K weight as for hqq_matmul.
+ * dX           M x K row-major: binary16 (out_f32 = 0; 2-byte aligned) or fp32 (out_f32 = 1;
+ *              4-byte aligned).
+ * workspace    hqq_matmul_backward_workspace_bytes(M, N, K) bytes of device memory, 16-byte
+ *              aligned, or NULL where that is 0: partial sums where few rows split N over
+ *              blocks.  Written and read on `stream`; calls that share it must be ordered.
+ * Conventions and errors as for hqq_quantize.
+ */
+int hqq_matmul_backward(const void* dY_f16, int64_t M, int64_t N, const void* packed_codes,
+                        const void* scale_f16, const void* zero_f16, int64_t K, int nbits,
+                        int group_size, void* dX, int out_f32, void* workspace, void* stream);
+
+/* Bytes of the workspace of hqq_matmul_backward (0: none needed); -1 for invalid shapes. */
+int64_t hqq_matmul_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Element types of the entry points below that take one. */
+enum {
+  HQQ_DTYPE_F16 = 0,  /* binary16 */
+  HQQ_DTYPE_BF16 = 1, /* bfloat16 */
+  HQQ_DTYPE_F32 = 2   /* binary32 */
+};
+
+/*
+ * hqq_expert_sort -- the (token, choice) slots of a routed layer in the order of their
+ * experts.  Slot s = t * topk + j is choice j of token t; ids[s] in [0, experts) names its
+ * expert, any other value drops it.  The sort is stable: the kept slots by expert, equal
+ * experts by slot, then the dropped slots by slot.
+ *   order[i]      the slot of sorted row i; ~slot (negative) for a dropped one;
+ *   position[s]   the sorted row of slot s; ~row for a dropped one;
+ *   offsets[e]    the first row of expert e; offsets[experts] the number of kept slots.
+ *
+ * ids_i32      tokens * topk int32.  tokens >= 0, topk >= 1, tokens * topk <= 2^31 - 1.
+ * experts      1 .. 1024 (above: HQQ_ERR_UNSUPPORTED).
+ * order_i32, position_i32   tokens * topk int32 each; offsets_i32  experts + 1 int32 (written
+ *              also without tokens).  All 4-byte aligned.
+ * workspace    hqq_expert_sort_workspace_bytes(tokens, topk, experts) bytes, 4-byte aligned, or
+ *              NULL where that is 0.  As for hqq_matmul.
+ * Conventions and errors as for hqq_quantize.
+ */
+int hqq_expert_sort(const void* ids_i32, int64_t tokens, int topk, int experts, void* order_i32,
+                    void* position_i32, void* offsets_i32, void* workspace, void* stream);
+
+/* Bytes of the workspace of hqq_expert_sort (0: none needed); -1 for invalid sizes. */
+int64_t hqq_expert_sort_workspace_bytes(int64_t tokens, int topk, int experts);
+
+/*
+ * hqq_expert_gather -- the tokens' rows in sorted order: Xs[position[s]] = X[s / topk], and
+ * zeros in the rows of dropped slots (the rows behind offsets[experts]).  Its gradient is
+ * hqq_expert_combine without weights.
+ * X            tokens x width elements of `dtype` (HQQ_DTYPE_*), row-major.
+ * position     as hqq_expert_sort writes it, for the same tokens and topk.
+ * Xs           (tokens * topk) x width elements.
+ * X and Xs aligned to their element (16-byte pieces are used where the width, X and Xs allow).
+ */
+int hqq_expert_gather(const void* X, int dtype, int64_t tokens, int topk, int64_t width,
+                      const void* position_i32, void* Xs, void* stream);
+
+/*
+ * hqq_expert_combine -- the way back: out[t] = sum over the kept choices j of token t of
+ * weights[t][j] * Ys[position[t * topk + j]], in fp32 in the order of the choices, rounded once.
+ * A token without kept choices gets zeros; the weights and rows of dropped choices are not
+ * used (they may hold anything).
+ * Ys           (tokens * topk) x width elements of `dtype`.
+ * weights_f32  tokens x topk fp32, or NULL: every weight is 1.
+ * out          tokens x width elements.
+ */
+int hqq_expert_combine(const void* Ys, int dtype, int64_t tokens, int topk, int64_t width,
+                       const void* position_i32, const void* weights_f32, void* out, void* stream);
+
+/*
+ * hqq_expert_combine_backward -- the gradients of hqq_expert_combine:
+ *   dYs[position[s]] = weights[s] * dOut[s / topk] (fp32, rounded once),
+ *   dweights[s]      = <dOut[s / topk], Ys[position[s]]> (fp32, in a fixed order),
+ * zeros in the rows and weights of dropped slots.
+ * dweights_f32 tokens x topk fp32, or NULL: not wanted (Ys may then be NULL).
+ */
+int hqq_expert_combine_backward(const void* dOut, const void* Ys, int dtype, int64_t tokens,
+                                int topk, int64_t width, const void* position_i32,
+                                const void* weights_f32, void* dYs, void* dweights_f32,
+                                void* stream);
+
+/*
+ * hqq_matmul_experts -- the products of sorted rows with the quantized weights of their
+ * experts: Y[i] = X[i] Q^-1(W_e)^T for the rows i in [offsets[e], offsets[e + 1]), and zeros in
+ * the rows behind offsets[experts].  The weights are one stored weight of experts * N rows
+ * and K columns (hqq_quantize of the stacked weights, or an arena of hqq_quantize_batch over
+ * equal shapes): expert e holds rows [e * N, (e + 1) * N).  Arithmetic as hqq_matmul: up to 8
+ * rows with 2-, 4- or 8-bit codes by its per-row path, more on the matrix cores.
+ *
+ * X_f16        the rows, K binary16 each, 16-byte aligned: sorted (order_i32 NULL: rows x K), or
+ *              the tokens (order_i32 as hqq_expert_sort writes it: row i is X[order[i] / topk];
+ *              rows = tokens * topk).
+ * rows         0 .. 8000000.  K a multiple of group_size and of 32.  K == 0 writes zeros.
+ * offsets_i32  experts + 1 int32 as hqq_expert_sort writes them.  experts 1 .. 1024.
+ * Y            rows x N binary16 or fp32 (out_f32).
+ * Other arguments, conventions and errors as for hqq_matmul.
+ */
+int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* order_i32, int topk,
+                       const void* offsets_i32, int experts, const void* packed_codes,
+                       const void* scale_f16, const void* zero_f16, int64_t N, int nbits,
+                       int group_size, void* Y, int out_f32, void* stream);
+
+/*
+ * hqq_matmul_experts_backward -- the gradient of hqq_matmul_experts' sorted rows: dX[i] =
+ * dY[i] Q^-1(W_e), zeros behind offsets[experts].  dY_f16 and dX are sorted rows (the tokens'
+ * gradient is hqq_expert_combine of dX without weights).  Arithmetic, arguments and errors as
+ * hqq_matmul_backward and hqq_matmul_experts; workspace of
+ * hqq_matmul_experts_backward_workspace_bytes(rows, N, K, experts) bytes.
+ */
+int hqq_matmul_experts_backward(const void* dY_f16, int64_t rows, int64_t N,
+                                const void* offsets_i32, int experts, const void* packed_codes,
+                                const void* scale_f16, const void* zero_f16, int64_t K, int nbits,
+                                int group_size, void* dX, int out_f32, void* workspace,
+                                void* stream);
+
+int64_t hqq_matmul_experts_backward_workspace_bytes(int64_t rows, int64_t N, int64_t K,
+                                                    int experts);
+
+/*
+ * hqq_adapters -- low-rank adapters of many requests beside one shared projection (for one
+ * quantized by hqq_quantize: base = hqq_matmul's Y).  Row m belongs to adapter a = ids[m]:
+ *   Y[m] = base[m] + scales[a] * B_a (A_a X[m])
+ * and Y[m] = base[m] where ids[m] is outside [0, adapters).  hqq_lowrank's factors, cast to 16
+ * bits, are one adapter of scale 1.  A_a X[m] is kept in fp32; up to 64 rows the sums are fp32
+ * dot products, above on the matrix cores, where A_a X[m] enters as two binary16 parts (22 bits
+ * of the row's largest value) or as bfloat16 parts (16 bits, 24 for an fp32 output).
+ *
+ * X            M x K elements of dtype HQQ_DTYPE_F16 or HQQ_DTYPE_BF16.  0 <= M <= 4000000.
+ * A            adapters x rank x K elements, B: adapters x N x rank elements, of `dtype`.
+ * N, K         > 0, K a multiple of 8.  rank a multiple of 8, up to 256 (else
+ *              HQQ_ERR_UNSUPPORTED; a smaller rank is padded with zeros).  adapters 1 .. 1024.
+ * ids_i32      M int32.  scales_f32: adapters fp32.
+ * base         M x N elements of `dtype` (base_f32 = 0) or fp32 (base_f32 = 1), or NULL: zeros.
+ *              It may be Y itself if they are of one type.
+ * Y            M x N elements of `dtype` (out_f32 = 0) or fp32 (out_f32 = 1), rounded once.
+ * workspace    hqq_adapters_workspace_bytes(M, N, K, rank, adapters) bytes of device memory,
+ *              256-byte aligned.  Written and read on `stream`; calls that share it must be
+ *              ordered.
+ * X, A, B 16-byte aligned; base and Y to their element.  M == 0 is a no-op.
+ * Conventions and errors as for hqq_quantize.
+ */
+int hqq_adapters(const void* X, int dtype, int64_t M, int64_t K, const void* A, const void* B,
+                 int64_t N, int rank, int adapters, const void* ids_i32, const void* scales_f32,
+                 const void* base, int base_f32, void* Y, int out_f32, void* workspace,
+                 void* stream);
+
+int64_t hqq_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters);
+
+/*
+ * hqq_adapters_backward -- the gradients of hqq_adapters:
+ *   dX[m] = base[m] + scales[a] * A_a^T (B_a^T dY[m])   (base[m] for rows of no adapter)
+ *   dA_a  = scales[a] * sum over its rows of (B_a^T dY[m]) X[m]^T
+ *   dB_a  = scales[a] * sum over its rows of dY[m] (A_a X[m])^T
+ * with dA and dB in fp32 (zeros for an adapter without rows), summed in an order that the
+ * shapes and ids fix.  For a quantized projection base is hqq_matmul_backward's dX.
+ *
+ * dY           M x N elements of `dtype`, 2-byte aligned.
+ * base         M x K elements of `dtype` or fp32 (base_f32), or NULL; it may be dX itself if
+ *              they are of one type.  dX: M x K elements of `dtype` or fp32 (out_f32).
+ * dA_f32       adapters x rank x K, dB_f32: adapters x N x rank fp32, 16-byte aligned.
+ * workspace    hqq_adapters_backward_workspace_bytes(M, N, K, rank, adapters) bytes, 256-byte
+ *              aligned.  M == 0 writes zeros to dA and dB.
+ * Other arguments, conventions and errors as for hqq_adapters.
+ */
+int hqq_adapters_backward(const void* dY, const void* X, int dtype, int64_t M, int64_t K,
+                          const void* A, const void* B, int64_t N, int rank, int adapters,
+                          const void* ids_i32, const void* scales_f32, const void* base,
+                          int base_f32, void* dX, int out_f32, void* dA_f32, void* dB_f32,
+                          void* workspace, void* stream);
+
+int64_t hqq_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank,
+                                              int adapters);
+
 /* Bytes of the packed code stream: rows*cols*nbits/8 (exact for supported
  * shapes).  Returns -1 for invalid arguments or overflow. */
 int64_t hqq_packed_bytes(int64_t rows, int64_t cols, int nbits);

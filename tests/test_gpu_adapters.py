@@ -1,0 +1,345 @@
+"""Low-rank adapters of many requests and their gradients on the GPU, against 64-bit formulas.
+
+fp32 results are held to fp32 accuracy (v and u enter the matrix cores as parts that add up to
+22 or 24 bits), 16-bit results to that and their own rounding.  Small integers pin indexing
+exactly, and exact differences pin the gradients.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+DTYPES = [torch.float16, torch.bfloat16]
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
+
+
+@pytest.fixture(scope="module")
+def hq():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm device")
+    import bit_weight_quantization_amd as m
+    m.load_library()
+    return m
+
+
+def _ids(M, n, none, seed):
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(0, n, M, dtype=np.int32)
+    wild = rng.choice(np.array([-1, n, 2 ** 31 - 1, -2 ** 31], np.int32), M)
+    return torch.from_numpy(np.where(rng.random(M) < none, wild, ids).astype(np.int32)).cuda()
+
+
+def _inputs(M, N, K, r, n, none, dtype, seed, ints=False):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def make(*shape, std=1.0):
+        if ints:
+            return torch.randint(-2, 3, shape, device="cuda", generator=gen).to(dtype)
+        return (torch.randn(shape, device="cuda", generator=gen) * std).to(dtype)
+    scales = torch.rand(n, device="cuda", generator=gen) + 0.5
+    if ints:
+        scales = 2.0 ** torch.randint(-1, 2, (n,), device="cuda", generator=gen).float()
+    return dict(X=make(M, K), A=make(n, r, K, std=K ** -0.5), B=make(n, N, r, std=0.1),
+                ids=_ids(M, n, none, seed), scales=scales), make
+
+
+def _rows(ids, a):
+    return torch.nonzero(ids == a)[:, 0]
+
+
+def _forward64(t, base=None):
+    """y and, elementwise, what its roundings scale with: (y, sum |B| |v|, sum |B| sum |A| |x|,
+    sum |B| max |v|)."""
+    X, A, B, ids = t["X"], t["A"], t["B"], t["ids"]
+    y = torch.zeros((X.shape[0], B.shape[1]), device="cuda", dtype=torch.float64)
+    y = y if base is None else base.double().clone()
+    mags = [torch.zeros_like(y) for _ in range(3)]
+    for a in range(A.shape[0]):
+        m = _rows(ids, a)
+        if not len(m):
+            continue
+        x, Aa, Ba, s = X[m].double(), A[a].double(), B[a].double(), float(t["scales"][a])
+        At, Bt = Aa.t().contiguous(), Ba.t().contiguous()
+        v = x @ At
+        y[m] += s * (v @ Bt)
+        mags[0][m] = s * (v.abs() @ Bt.abs())
+        mags[1][m] = s * (x.abs() @ At.abs() @ Bt.abs())
+        mags[2][m] = s * v.abs().amax(1, keepdim=True) * Ba.abs().sum(1)[None]
+    return y, mags
+
+
+def _forward_bound(t, y, mags, base, out_f32):
+    """v: fp32 sums over K; its parts: 22 bits of the row's largest value (binary16) or 16 bits of
+    each value (bfloat16 under a 16-bit result; 24 under fp32); fp32 sums over the parts of the
+    rank; the scale, the base and the result one rounding each."""
+    K, r, dtype = t["X"].shape[1], t["A"].shape[1], t["X"].dtype
+    parts = mags[2] * 2.0 ** -22 if dtype == torch.float16 else mags[0] * (2.0 ** -24 if out_f32 else 2.0 ** -16)
+    b = (K + 8) * U32 * mags[1] + parts + (3 * r + 8) * U32 * mags[0]
+    b = b + 4 * U32 * (mags[0] + (0 if base is None else base.double().abs()))
+    return b if out_f32 else b + torch.finfo(dtype).eps / 2 * (y.abs() + b) + TINY[dtype]
+
+
+# rows, N, K, rank, adapters, none: one row, few rows, the last few and the first many; ragged N
+# and K of every kind; ranks up to 256; more adapters than rows; no adapter at all
+SHAPES = [(1, 130, 64, 8, 1, 0.0), (3, 1, 8, 16, 4, 0.3), (17, 515, 520, 24, 3, 0.2),
+          (64, 1000, 1032, 40, 9, 0.1), (65, 1001, 1032, 40, 9, 0.1), (66, 64, 136, 256, 2, 0.0),
+          (100, 130, 2056, 64, 300, 0.1), (300, 257, 384, 128, 5, 0.2), (1000, 300, 512, 16, 3, 0.0),
+          (130, 77, 72, 8, 2, 1.0), (500, 1111, 256, 72, 1, 0.5)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K,r,n,none", SHAPES)
+def test_forward(hq, M, N, K, r, n, none, dtype):
+    t, make = _inputs(M, N, K, r, n, none, dtype, seed=M + N)
+    b16, b32 = make(M, N), torch.randn((M, N), device="cuda")
+    for base in (None, b16, b32):
+        y, mags = _forward64(t, base)
+        for out_f32 in (False, True):
+            got = hq.adapters(**t, base=base, out_f32=out_f32).double()
+            bound = _forward_bound(t, y, mags, base, out_f32)
+            assert bool(((got - y).abs() <= bound).all()), (out_f32, float(((got - y).abs() / bound).max()))
+    mine = b16.clone()  # in place
+    assert hq.adapters(**t, base=mine, out=mine) is mine
+    assert torch.equal(mine, hq.adapters(**t, base=b16))
+    none_of = (t["ids"] < 0) | (t["ids"] >= n)
+    assert torch.equal(mine[none_of], b16[none_of])
+
+
+def _backward64(t, dY, base):
+    X, A, B, ids = t["X"], t["A"], t["B"], t["ids"]
+    dX = torch.zeros(X.shape, device="cuda", dtype=torch.float64) if base is None else base.double().clone()
+    dA, dB = torch.zeros_like(A, dtype=torch.float64), torch.zeros_like(B, dtype=torch.float64)
+    mA, mB = torch.zeros_like(dA), torch.zeros_like(dB)
+    for a in range(A.shape[0]):
+        m = _rows(ids, a)
+        if not len(m):
+            continue
+        x, d, Aa, Ba, s = X[m].double(), dY[m].double(), A[a].double(), B[a].double(), float(t["scales"][a])
+        u, v = d @ Ba, x @ Aa.t().contiguous()
+        au, av = d.abs() @ Ba.abs(), x.abs() @ Aa.t().contiguous().abs()
+        dX[m] += s * (u @ Aa)
+        dA[a] = s * (u.t().contiguous() @ x)
+        dB[a] = s * (d.t().contiguous() @ v)
+        N, K, R = d.shape[1], x.shape[1], len(m)
+        # u and v: fp32 sums (N or K long); 22 bits of the adapter's largest; fp32 sums over rows
+        eu = (N + 8) * U32 * au + 2.0 ** -22 * u.abs().max()
+        ev = (K + 8) * U32 * av + 2.0 ** -22 * v.abs().max()
+        mA[a] = s * ((eu + (3 * R + 8) * U32 * u.abs()).t().contiguous() @ x.abs())
+        mB[a] = s * (d.abs().t().contiguous() @ (ev + (3 * R + 8) * U32 * v.abs()))
+    return dX, dA, dB, mA, mB
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K,r,n,none", SHAPES + [(5000, 130, 72, 16, 2, 0.1)])
+def test_backward(hq, M, N, K, r, n, none, dtype):
+    t, make = _inputs(M, N, K, r, n, none, dtype, seed=M + K)
+    dY, b16, b32 = make(M, N), make(M, K), torch.randn((M, K), device="cuda")
+    for base in (None, b16, b32):
+        dX, dA, dB, mA, mB = _backward64(t, dY, base)
+        # dx is the forward with the factors' places swapped
+        sw = dict(X=dY, A=t["B"].transpose(1, 2), B=t["A"].transpose(1, 2), ids=t["ids"], scales=t["scales"])
+        y, mags = _forward64(sw, base)
+        for out_f32 in (False, True):
+            gX, gA, gB = hq.adapters_backward(dY, **t, base=base, out_f32=out_f32)
+            assert bool(((gX.double() - dX).abs() <= _forward_bound(sw, y, mags, base, out_f32)).all())
+            assert bool(((gA.double() - dA).abs() <= mA + 1e-30).all()), float(((gA.double() - dA).abs() / (mA + 1e-30)).max())
+            assert bool(((gB.double() - dB).abs() <= mB + 1e-30).all()), float(((gB.double() - dB).abs() / (mB + 1e-30)).max())
+    used = torch.zeros(n, dtype=torch.bool, device="cuda")
+    ids = t["ids"]
+    used[ids[(ids >= 0) & (ids < n)].long()] = True
+    assert bool((gA[~used] == 0).all()) and bool((gB[~used] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_exact_on_small_integers(hq, M, dtype):
+    """Values that every part and sum holds exactly (|v| <= 4 * 40 and so on, far below 2^24)."""
+    t, make = _inputs(M, 75, 40, 24, 5, 0.2, dtype, seed=M, ints=True)
+    dY = make(M, 75)
+    y, _ = _forward64(t)
+    assert torch.equal(hq.adapters(**t, out_f32=True).double(), y)
+    dX, dA, dB, _, _ = _backward64(t, dY, None)
+    gX, gA, gB = hq.adapters_backward(dY, **t, out_f32=True)
+    assert torch.equal(gX.double(), dX) and torch.equal(gA.double(), dA) and torch.equal(gB.double(), dB)
+
+
+@pytest.mark.parametrize("M", [9, 200])
+def test_gradients_agree_with_differences(hq, M):
+    """y is linear in X, in A and in B: exact differences on small integers."""
+    t, make = _inputs(M, 50, 64, 16, 3, 0.1, torch.bfloat16, seed=M, ints=True)
+    g = make(M, 50)
+    dX, dA, dB = hq.adapters_backward(g, **t, out_f32=True)
+    y = hq.adapters(**t, out_f32=True).double()
+    for name, grad in (("X", dX), ("A", dA), ("B", dB)):
+        step = make(*t[name].shape)
+        moved = hq.adapters(**{**t, name: t[name] + step}, out_f32=True).double()
+        assert float((g.double() * (moved - y)).sum()) == float((grad.double() * step.double()).sum()), name
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M", [20, 400])
+def test_rows_without_adapter_may_hold_anything(hq, M, dtype):
+    """NaN and infinities in rows of no adapter, and in adapters of no row, reach no result."""
+    t, make = _inputs(M, 96, 128, 16, 4, 0.0, dtype, seed=M)
+    t["ids"] = torch.where(t["ids"] == 2, torch.full_like(t["ids"], -1), t["ids"])
+    dY = make(M, 96)
+    clean = (hq.adapters(**t), *hq.adapters_backward(dY, **t))
+    off = t["ids"] < 0
+    bad = dict(t, X=t["X"].clone(), A=t["A"].clone(), B=t["B"].clone(), scales=t["scales"].clone())
+    bad["X"][off], bad["A"][2], bad["B"][2] = float("nan"), float("inf"), float("nan")
+    bad["scales"][2] = float("nan")
+    dYb = dY.clone()
+    dYb[off] = float("-inf")
+    got = (hq.adapters(**bad), *hq.adapters_backward(dYb, **bad))
+    for a, b in zip(got, clean):
+        assert torch.equal(a, b)
+
+
+def test_an_infinite_factor_row_stays_in_its_own_rank(hq):
+    """One infinite value of A makes that rank's dB column infinite or NaN and nothing else."""
+    t, make = _inputs(300, 64, 128, 16, 1, 0.0, torch.float16, seed=1)
+    dY = make(300, 64)
+    _, _, clean = hq.adapters_backward(dY, **t)
+    t["A"][0, 5, 7] = float("inf")
+    _, _, dB = hq.adapters_backward(dY, **t)
+    keep = torch.arange(16, device="cuda") != 5
+    assert not bool(dB[0][:, 5].isfinite().any())
+    assert torch.equal(dB[0][:, keep], clean[0][:, keep])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_small_and_large_gradients_keep_their_digits(hq, dtype):
+    """u far below and above binary16's range: the parts are scaled, so dA keeps fp32 accuracy."""
+    t, make = _inputs(300, 64, 128, 16, 2, 0.0, dtype, seed=3)
+    for factor in (2.0 ** -14, 2.0 ** 10):
+        dY = (make(300, 64).float() * factor).to(dtype)
+        big = dict(t, B=(t["B"].float() * factor).to(dtype))
+        _, dA, dB, mA, mB = _backward64(big, dY, None)
+        _, gA, gB = hq.adapters_backward(dY, **big)
+        assert bool(((gA.double() - dA).abs() <= mA).all()) and bool(((gB.double() - dB).abs() <= mB).all())
+        assert float((gA.double() - dA).norm() / dA.norm()) < 2e-6
+
+
+def test_no_rows(hq):
+    t, _ = _inputs(0, 64, 128, 16, 3, 0.0, torch.float16, seed=1)
+    assert hq.adapters(**t).shape == (0, 64)
+    dX, dA, dB = hq.adapters_backward(torch.empty((0, 64), device="cuda", dtype=torch.float16), **t)
+    assert dX.shape == (0, 128) and not bool(dA.any()) and not bool(dB.any())
+
+
+def _quantized(hq, N, K, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    W = (torch.randn((N, K), device="cuda", generator=gen) * 0.05).half()
+    return W, hq.quantize(W, 4, 64)
+
+
+@pytest.mark.parametrize("M", [1, 2, 12, 40, 64, 90, 600])
+def test_adapters_of_a_quantized_projection_and_the_gradients(hq, M):
+    """The combined calls against 64 bits of the stored weight: binary16 results, off by their own
+    rounding and the weight's (relative 2-norm under 2^-10 together)."""
+    N, K = 384, 512
+    _, q = _quantized(hq, N, K, 1)
+    Wd = q.scale.double().repeat_interleave(64, 1)
+    codes = torch.stack([(q.packed & 15), (q.packed >> 4)], 1).view(N, K).double()
+    Wd = Wd * (codes - q.zero.double().repeat_interleave(64, 1))
+    t, make = _inputs(M, N, K, 16, 5, 0.2, torch.float16, seed=M)
+    dY = make(M, N)
+    y, _ = _forward64(t, t["X"].double() @ Wd.t().contiguous())
+    dX, dA, dB, mA, mB = _backward64(t, dY, dY.double() @ Wd)
+    got = hq.matmul_adapters(t["X"], q, t["A"], t["B"], t["ids"], t["scales"])
+    assert float((got.double() - y).norm() / y.norm()) < 2.0 ** -10
+    gX, gA, gB = hq.matmul_adapters_backward(dY, t["X"], q, t["A"], t["B"], t["ids"], t["scales"])
+    assert float((gX.double() - dX).norm() / dX.norm()) < 2.0 ** -10
+    assert bool(((gA.double() - dA).abs() <= mA).all()) and bool(((gB.double() - dB).abs() <= mB).all())
+
+
+def test_factors_of_the_lowrank_compensation_serve_as_an_adapter(hq):
+    """hqq_lowrank's factors beside the quantized product come closer to the full weight's product
+    than the quantized product alone, for the requests that use them, and change no other."""
+    W, q = _quantized(hq, 512, 512, 2)
+    W[:, :8] *= 8  # a part of low rank in the error
+    q = hq.quantize(W, 2, 64)
+    B, A, _ = hq.lowrank(W, q, rank=32)
+    X = torch.randn((100, 512), device="cuda").half()
+    ids = torch.arange(100, device="cuda", dtype=torch.int32) % 2 - 1  # -1, 0, -1, ...
+    one = torch.ones(1, device="cuda")
+    y = hq.matmul_adapters(X, q, A.half()[None].contiguous(), B.half()[None].contiguous(), ids, one).double()
+    want = X.double() @ W.double().t().contiguous()
+    plain = hq.matmul(X, q, out_f32=True).half().double()
+    assert torch.equal(y[0::2], plain[0::2])
+    assert float((y[1::2] - want[1::2]).norm()) < 0.97 * float((plain[1::2] - want[1::2]).norm())
+
+
+@pytest.mark.parametrize("M", [30, 500])
+def test_captured_step_replays_and_repeats(hq, M):
+    """A training step captured into a graph, replayed with new inputs and eager work between the
+    replays, equals the eager result bit for bit."""
+    _, q = _quantized(hq, 384, 512, 1)
+    held, make = _inputs(M, 384, 512, 16, 5, 0.2, torch.float16, seed=M)
+    dY = make(M, 384)
+
+    def step(t, dY):
+        return (hq.matmul_adapters(t["X"], q, t["A"], t["B"], t["ids"], t["scales"]),
+                *hq.matmul_adapters_backward(dY, t["X"], q, t["A"], t["B"], t["ids"], t["scales"]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(held, dY)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(held, dY)
+    for i in range(4):
+        new, make = _inputs(M, 384, 512, 16, 5, 0.2, torch.float16, seed=M + i + 1)
+        for k in held:
+            held[k].copy_(new[k])
+        newY = make(M, 384)
+        dY.copy_(newY)
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = [g.clone() for g in got]
+        eager = step(new, newY)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(mine, eager))
+
+
+def test_two_streams_at_once(hq):
+    """Calls with workspaces of their own on two streams give the results of calls in turn."""
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ts = [_inputs(700, 512, 1024, 32, 3, 0.1, torch.bfloat16, seed=i) for i in range(2)]
+    dYs = [make(700, 512) for _, make in ts]
+    want = [(hq.adapters(**t), *hq.adapters_backward(d, **t)) for (t, _), d in zip(ts, dYs)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i in range(2):
+            got[i] = (hq.adapters(**ts[i][0], stream=s[i]),
+                      *hq.adapters_backward(dYs[i], **ts[i][0], stream=s[i]))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_tensor_refusals(hq):
+    t, make = _inputs(6, 64, 128, 16, 3, 0.0, torch.float16, seed=1)
+    for name, bad in (("X", t["X"].float()), ("X", t["X"].bfloat16()), ("X", t["X"][:, :64]),
+                      ("A", t["A"][:, :8]), ("A", t["A"].float()), ("B", t["B"].transpose(1, 2)),
+                      ("ids", t["ids"].long()), ("ids", t["ids"][:5]), ("scales", t["scales"].half()),
+                      ("scales", t["scales"][:2]), ("ids", t["ids"].cpu())):
+        with pytest.raises(ValueError):
+            hq.adapters(**{**t, name: bad})
+    for base in (make(6, 63), make(6, 64).bfloat16(), make(6, 64).double()):
+        with pytest.raises(ValueError):
+            hq.adapters(**t, base=base)
+    same = torch.zeros((6, 64), device="cuda")
+    with pytest.raises(ValueError):
+        hq.adapters(**t, base=same, out=same)  # float32 base in place of a float16 result
+    with pytest.raises(ValueError):
+        hq.adapters(**t, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        hq.adapters_backward(make(6, 32), **t)
+    thin = dict(t, A=t["A"][:, :12].contiguous(), B=t["B"][:, :, :12].contiguous())
+    with pytest.raises(hq.HQQError):
+        hq.adapters(**thin)

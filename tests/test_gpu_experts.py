@@ -1,0 +1,421 @@
+"""The order of experts, the quantized experts' products and the gradients of a product with a
+quantized weight on the GPU, against plain 64-bit formulas.
+
+Integer results are compared for equality.  Products are pinned by exact cases (scales powers of
+two, integer zero-points, small integer rows: every product and partial sum is exact in fp32
+whatever its order) over all widths, group sizes and row counts of every path, and bounded on
+general inputs by the arithmetic of the matrix-core path.
+"""
+import numpy as np
+import pytest
+
+import oracle
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U32, U16 = 2.0 ** -24, 2.0 ** -11
+DTYPES = [torch.float16, torch.bfloat16, torch.float32]
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126, torch.float32: 2.0 ** -126}
+
+
+@pytest.fixture(scope="module")
+def hq():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm device")
+    import bit_weight_quantization_amd as m
+    m.load_library()
+    return m
+
+
+def _plain_order(ids, experts):
+    """order, position, offsets of flat numpy ids: kept slots stable by expert, dropped ones last."""
+    key = np.where((ids >= 0) & (ids < experts), ids, experts)
+    order = np.argsort(key, kind="stable")
+    position = np.empty_like(order)
+    position[order] = np.arange(ids.size)
+    kept = int((key < experts).sum())
+    code = np.where(np.arange(ids.size) < kept, order, ~order)
+    position = np.where(position < kept, position, ~position)
+    offsets = np.searchsorted(key[order], np.arange(experts + 1))
+    return code, position, offsets
+
+
+def _ids(tokens, topk, experts, dropped, seed):
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(0, experts, (tokens, topk), dtype=np.int32)
+    wild = rng.choice(np.array([-1, experts, 2 ** 31 - 1, -2 ** 31], np.int32), ids.shape)
+    return np.where(rng.random(ids.shape) < dropped, wild, ids).astype(np.int32)
+
+
+@pytest.mark.parametrize("tokens,topk,experts,dropped", [
+    (0, 2, 8, 0), (1, 1, 1, 0), (1, 1, 1, 1), (1, 2, 8, 0), (3, 5, 7, 0.5), (63, 1, 64, 0.1),
+    (65, 1, 1024, 0), (512, 8, 64, 0.1), (4096, 1, 1000, 0.5), (4097, 1, 63, 0.1), (700, 6, 256, 0),
+    (9000, 8, 128, 0.2), (300001, 1, 1024, 0.01), (5000, 2, 3, 1), (1 << 20, 2, 5, 0.3)])
+def test_sort_is_the_stable_order(hq, tokens, topk, experts, dropped):
+    ids = _ids(tokens, topk, experts, dropped, tokens + experts)
+    r = hq.expert_sort(torch.from_numpy(ids).cuda(), experts)
+    want = _plain_order(ids.ravel(), experts)
+    for got, w in zip((r.order, r.position, r.offsets), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+
+
+def _route(hq, tokens, topk, experts, dropped, seed):
+    ids = _ids(tokens, topk, experts, dropped, seed)
+    r = hq.expert_sort(torch.from_numpy(ids).cuda(), experts)
+    order = r.order.cpu().numpy()
+    return r, order, np.where(order < 0, ~order, order)
+
+
+ROWS = [(1, 1, 1, 0.0), (1, 2, 64, 0.0), (5, 3, 7, 0.4), (33, 8, 4096, 0.1), (17, 9, 1001, 0.3),
+        (64, 2, 24, 1.0), (300, 17, 130, 0.2), (2, 2, 20000, 0.0)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,topk,width,dropped", ROWS)
+def test_gather_moves_rows_and_clears_dropped_ones(hq, tokens, topk, width, dropped, dtype):
+    r, order, slot = _route(hq, tokens, topk, 6, dropped, width)
+    X = torch.randn((tokens, width), device="cuda").to(dtype)
+    out = torch.full((tokens * topk, width), float("nan"), device="cuda", dtype=dtype)
+    assert hq.expert_gather(X, r, out=out) is out
+    want = X[torch.from_numpy(slot // topk).cuda()]
+    want[torch.from_numpy(order < 0).cuda()] = 0
+    assert torch.equal(out, want)
+
+
+def _round_bound(dtype, y):
+    return torch.finfo(dtype).eps / 2 * y.abs() + TINY[dtype]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,topk,width,dropped", ROWS)
+def test_combine_and_its_gradients(hq, tokens, topk, width, dropped, dtype):
+    """Dropped slots' weights and rows hold NaN, which must not reach any result."""
+    r, order, slot = _route(hq, tokens, topk, 6, dropped, width + 1)
+    gen = torch.Generator(device="cuda").manual_seed(width)
+    gone = torch.from_numpy(order < 0).cuda()
+    slot_t = torch.from_numpy(slot).cuda()
+    Ys = torch.randn((tokens * topk, width), device="cuda", generator=gen).to(dtype)
+    w = torch.randn(tokens * topk, device="cuda", generator=gen)
+    dOut = torch.randn((tokens, width), device="cuda", generator=gen).to(dtype)
+    Ysn, wn = Ys.clone(), w.clone()
+    Ysn[gone] = float("nan")
+    wn[slot_t[gone]] = float("nan")
+
+    y64, w64 = Ys.double(), w.double()[slot_t]
+    y64[gone] = 0
+    w64[gone] = 0
+    token = slot_t // topk
+    want = torch.zeros((tokens, width), device="cuda", dtype=torch.float64)
+    mag = torch.zeros_like(want)
+    want.index_add_(0, token, w64[:, None] * y64)
+    mag.index_add_(0, token, (w64[:, None] * y64).abs())
+    got = hq.expert_combine(Ysn, r, wn.view(tokens, topk))
+    err = (got.double() - want).abs()
+    # one fused multiply-add per choice, each off by at most U32 of a partial sum, then one rounding
+    bound = topk * U32 * mag
+    assert bool((err <= bound + _round_bound(dtype, want.abs() + bound)).all())
+
+    ones = hq.expert_combine(Ysn, r)  # weights of 1
+    plain = torch.zeros_like(want)
+    plain.index_add_(0, token, y64)
+    mag1 = torch.zeros_like(want)
+    mag1.index_add_(0, token, y64.abs())
+    b1 = topk * U32 * mag1
+    assert bool(((ones.double() - plain).abs() <= b1 + _round_bound(dtype, plain.abs() + b1)).all())
+
+    dYs, dw = hq.expert_combine_backward(dOut, Ysn, r, wn.view(tokens, topk))
+    d64 = dOut.double()[token]
+    wantY = w64[:, None] * d64
+    # the fp32 product (U32), then the type's rounding
+    assert bool(((dYs.double() - wantY).abs() <= U32 * wantY.abs() + _round_bound(dtype, wantY * (1 + U32))).all())
+    assert bool((dYs[gone] == 0).all())
+    wantw = torch.zeros(tokens * topk, device="cuda", dtype=torch.float64)
+    magw = torch.zeros_like(wantw)
+    wantw[slot_t] = (d64 * y64).sum(1)
+    magw[slot_t] = (d64 * y64).abs().sum(1)
+    # width / 64 fused multiply-adds a lane at least, then 6 + 2 sums; at most `width` roundings
+    assert bool(((dw.view(-1).double() - wantw).abs() <= (width + 8) * U32 * magw).all())
+    only, none = hq.expert_combine_backward(dOut, None, r)
+    assert none is None
+    assert torch.equal(only[~gone], dOut[token][~gone]) and bool((only[gone] == 0).all())
+
+
+def test_rows_of_any_alignment(hq):
+    """Widths and pointers that are not multiples of 16 bytes: rows of a shifted buffer."""
+    r, order, slot = _route(hq, 9, 2, 6, 0.2, 3)
+    keep = torch.from_numpy(order >= 0).cuda()[:, None]
+    for width in (8, 9, 64):
+        flat = torch.randn(9 * width + 1, device="cuda").half()
+        X = flat[1:].view(9, width)
+        out = torch.empty(18 * width + 1, device="cuda", dtype=torch.float16)[1:].view(18, width)
+        hq.expert_gather(X, r, out=out)
+        want = torch.where(keep, X[torch.from_numpy(slot // 2).cuda()], torch.zeros((), device="cuda").half())
+        assert torch.equal(out, want)
+        back = hq.expert_combine(out, r)
+        n = torch.zeros(9, device="cuda").index_add_(0, torch.from_numpy(slot // 2).cuda(), keep[:, 0].float())
+        assert torch.equal(back, (X.float() * n[:, None]).half())
+
+
+def test_combine_gradients_agree_with_differences(hq):
+    """combine is linear in the rows and in the weights: on small integers in float32 its exact
+    differences equal the gradients' products with the direction."""
+    r, order, slot = _route(hq, 40, 4, 6, 0.2, 11)
+    rng = torch.Generator(device="cuda").manual_seed(5)
+
+    def ints(*shape):
+        return torch.randint(-4, 5, shape, device="cuda", generator=rng).float()
+    Y, dY, w, dw, g = ints(160, 96), ints(160, 96), ints(40, 4), ints(40, 4), ints(40, 96)
+    gY, gw = hq.expert_combine_backward(g, Y, r, w)
+    f = hq.expert_combine
+    assert float((g * (f(Y + dY, r, w) - f(Y, r, w))).sum()) == float((gY * dY).sum())
+    assert float((g * (f(Y, r, w + dw) - f(Y, r, w))).sum()) == float((gw * dw).sum())
+    X, dX = ints(40, 96), ints(40, 96)
+    gx = hq.expert_combine(dY, r)  # the gather's gradient
+    moved = hq.expert_gather(X + dX, r) - hq.expert_gather(X, r)
+    assert float((dY * moved).sum()) == float((gx * dX).sum())
+
+
+# ---------------------------------------------------------------- products --
+
+def _weight(rows, K, nbits, g, seed, exact):
+    rng = np.random.default_rng(seed)
+    qmax = (1 << nbits) - 1
+    codes = rng.integers(0, qmax + 1, (rows, K), dtype=np.uint8)
+    if exact:
+        s = (2.0 ** -rng.integers(3, 7, (rows, K // g))).astype(np.float16)
+        z = rng.integers(0, qmax + 1, (rows, K // g)).astype(np.float16)
+    else:
+        s = np.asarray(rng.uniform(2e-4, 4e-3, (rows, K // g)), np.float16)
+        z = np.asarray(rng.uniform(-0.5, qmax + 0.5, (rows, K // g)), np.float16)
+    return codes, oracle.pack_codes(codes.ravel(), nbits), s, z
+
+
+def _quantized(hq, rows, K, nbits, g, seed, exact=True):
+    """A stored weight on the device and its exact 64-bit value."""
+    codes, packed, s, z = _weight(rows, K, nbits, g, seed, exact)
+    q = hq.QuantizedWeight(packed=torch.from_numpy(packed).cuda(), scale=torch.from_numpy(s).cuda(),
+                           zero=torch.from_numpy(z).cuda(), rows=rows, cols=K, nbits=nbits, group_size=g)
+    s64 = torch.from_numpy(s).cuda().double().repeat_interleave(g, 1)
+    z64 = torch.from_numpy(z).cuda().double().repeat_interleave(g, 1)
+    return q, s64 * (torch.from_numpy(codes).cuda().double() - z64)
+
+
+def _ints(shape, seed, lim=2):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-lim, lim + 1, shape, device="cuda", generator=gen).half()
+
+
+def _want(rows, W, offsets, N, transposed):
+    """Row by row product with the weight of the row's expert, 64 bits; zeros behind the last."""
+    out = torch.zeros((rows.shape[0], W.shape[1] if transposed else N), device="cuda", dtype=torch.float64)
+    for e in range(len(offsets) - 1):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if b > a:
+            We = W[e * N:(e + 1) * N]
+            out[a:b] = rows[a:b].double() @ (We if transposed else We.t().contiguous())
+    return out
+
+
+WIDTHS = [(4, 64), (2, 32), (2, 16), (3, 32), (8, 128), (4, 16), (3, 128), (8, 32)]
+# tokens, topk, experts, N, K, dropped: a row each (<= 8 rows); 16, 32 and 64 rows a tile; 128 and
+# 256; ragged N; K that is and is not a multiple of 256; more experts than rows
+SHAPES = [(1, 2, 8, 300, 256, 0.0), (4, 2, 3, 70, 384, 0.4), (8, 1, 16, 8200, 256, 0.0),
+          (10, 2, 5, 33, 640, 0.1), (40, 2, 9, 130, 512, 0.0), (50, 3, 8, 4100, 256, 0.2),
+          (100, 3, 8, 129, 768, 0.1), (150, 2, 2, 257, 256, 0.0), (700, 1, 2, 140, 384, 0.3)]
+
+
+@pytest.mark.parametrize("nbits,g", WIDTHS)
+def test_experts_products_and_gradients_are_exact_on_exact_inputs(hq, nbits, g):
+    for tokens, topk, E, N, K, dropped in SHAPES:
+        r, order, slot = _route(hq, tokens, topk, E, dropped, tokens + N)
+        offsets = r.offsets.cpu().numpy()
+        q, W = _quantized(hq, E * N, K, nbits, g, seed=N + K)
+        X = _ints((tokens, K), seed=tokens)
+        Xs = hq.expert_gather(X, r)
+        want = _want(Xs, W, offsets, N, False)
+        assert torch.equal(hq.matmul_experts(X, q, r, out_f32=True).double(), want), (tokens, N, K)
+        assert torch.equal(hq.matmul_experts(Xs, q, r, sorted_rows=True), want.half()), (tokens, N, K)
+        dY = _ints((r.rows, N), seed=tokens + 1)
+        want = _want(dY, W, offsets, N, True)
+        assert torch.equal(hq.matmul_experts_backward(dY, q, r, out_f32=True).double(), want), (tokens, N, K)
+        assert torch.equal(hq.matmul_experts_backward(dY, q, r), want.half()), (tokens, N, K)
+
+
+@pytest.mark.parametrize("nbits,g", WIDTHS)
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (3, 7, 256), (5, 1000, 384), (64, 2500, 128),
+                                   (129, 63, 640), (300, 65, 256), (257, 515, 1152)])
+def test_gradient_of_the_product_is_exact_on_exact_inputs(hq, nbits, g, M, N, K):
+    q, W = _quantized(hq, N, K, nbits, g, seed=N + K)
+    dY = _ints((M, N), seed=M)
+    want = dY.double() @ W
+    assert torch.equal(hq.matmul_backward(dY, q, out_f32=True).double(), want)
+    assert torch.equal(hq.matmul_backward(dY, q), want.half())
+
+
+def _bound(x, W, out_f32, y):
+    """Matrix-core path: each weight rounded to fp32 and binary16 (U16 + 2 U32 relative, 2^-25
+    absolute for subnormals), fp32 sums over the contraction, the output's rounding."""
+    n = W.shape[0]
+    ax, aw = x.double().abs(), W.abs()
+    b = ax @ ((U16 + 2 * U32) * aw + 2.0 ** -25) + (n + 8) * U32 * (1 + 2 * U16) * (ax @ aw)
+    return b if out_f32 else b + U16 * y.abs() + 2.0 ** -25
+
+
+@pytest.mark.parametrize("nbits,g", [(4, 64), (2, 32), (3, 16), (8, 128)])
+@pytest.mark.parametrize("M", [2, 40, 300])
+def test_general_inputs_within_the_bound(hq, nbits, g, M):
+    N, K, E = 515, 640, 3
+    q, W = _quantized(hq, N * E, K, nbits, g, seed=M, exact=False)
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    r, _, _ = _route(hq, M, 1, E, 0.1, M)
+    dY = torch.randn((M, N), device="cuda", generator=gen).half()
+    X = torch.randn((M, K), device="cuda", generator=gen).half()
+    offsets = r.offsets.cpu().numpy()
+    for out_f32 in (True, False):
+        dX = hq.matmul_experts_backward(dY, q, r, out_f32=out_f32).double()
+        Y = hq.matmul_experts(X, q, r, out_f32=out_f32).double()
+        Xs = hq.expert_gather(X, r)
+        for e in range(E):
+            a, b = int(offsets[e]), int(offsets[e + 1])
+            We = W[e * N:(e + 1) * N]
+            want = dY[a:b].double() @ We
+            assert bool(((dX[a:b] - want).abs() <= _bound(dY[a:b], We, out_f32, want)).all())
+            Wt = We.t().contiguous()
+            want = Xs[a:b].double() @ Wt
+            # (up to 8 rows: exact codes, 16 at a time, s (p - z sum x) in fp32)
+            few = (K / 16 + 30) * U32 * (Xs[a:b].double().abs() @ (Wt.abs() + 2 * Wt.abs().max()))
+            assert bool(((Y[a:b] - want).abs() <= _bound(Xs[a:b], Wt, out_f32, want) + few).all())
+        assert bool((dX[int(offsets[E]):] == 0).all()) and bool((Y[int(offsets[E]):] == 0).all())
+
+
+def test_every_row_of_one_expert_and_rows_that_hold_nan(hq):
+    """All tokens on the last of many experts (the others empty), and a NaN row that must stay in
+    its own results."""
+    N, K, E = 100, 256, 40
+    q, W = _quantized(hq, E * N, K, 4, 64, seed=1)
+    for tokens in (3, 60, 200):
+        ids = torch.full((tokens, 1), E - 1, dtype=torch.int32, device="cuda")
+        ids[0, 0] = 2
+        r = hq.expert_sort(ids, E)
+        X = _ints((tokens, K), seed=tokens)
+        X[0] = float("nan")
+        dY = _ints((tokens, N), seed=tokens + 1)
+        dY[0] = float("nan")  # sorted row 0: the only row of expert 2
+        Y, dX = hq.matmul_experts(X, q, r), hq.matmul_experts_backward(dY, q, r)
+        assert bool(Y[0].isnan().all()) and bool(dX[0].isnan().all())
+        We = W[(E - 1) * N:]
+        assert torch.equal(Y[1:], (X[1:].double() @ We.t().contiguous()).half())
+        assert torch.equal(dX[1:], (dY[1:].double() @ We).half())
+
+
+def _layer(hq, X, ids, w, q_up, q_down, dOut):
+    """A routed layer of two products and its gradients, as a program runs them."""
+    r = hq.expert_sort(ids, 6)
+    H = hq.matmul_experts(X, q_up, r)
+    Y = hq.matmul_experts(H, q_down, r, sorted_rows=True)
+    out = hq.expert_combine(Y, r, w)
+    dY, dw = hq.expert_combine_backward(dOut, Y, r, w)
+    dH = hq.matmul_experts_backward(dY, q_down, r)
+    dXs = hq.matmul_experts_backward(dH, q_up, r)
+    return out, hq.expert_combine(dXs, r), dw
+
+
+def test_a_routed_layer_forward_and_backward(hq):
+    """The operators together against 64-bit formulas: relative 2-norm errors at most those of
+    the roundings on the way (weights and four tensors at half a binary16 step each: < 2^-8)."""
+    T, k, E, D, F = 130, 2, 6, 256, 384
+    q_up, Wu = _quantized(hq, E * F, D, 4, 64, seed=1, exact=False)
+    q_down, Wd = _quantized(hq, E * D, F, 2, 32, seed=2, exact=False)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn((T, D), device="cuda", generator=gen).half()
+    w = torch.rand((T, k), device="cuda", generator=gen)
+    dOut = torch.randn((T, D), device="cuda", generator=gen).half()
+    ids = torch.from_numpy(_ids(T, k, E, 0.1, 4)).cuda()
+    out, dX, dw = _layer(hq, X, ids, w, q_up, q_down, dOut)
+    want, wx, ww = torch.zeros_like(X).double(), torch.zeros_like(X).double(), torch.zeros_like(w).double()
+    for j in range(k):
+        for e in range(E):
+            rows = torch.nonzero(ids[:, j] == e)[:, 0]
+            U, V = Wu[e * F:(e + 1) * F], Wd[e * D:(e + 1) * D]
+            y = X[rows].double() @ U.t().contiguous() @ V.t().contiguous()
+            want[rows] += w[rows, j, None].double() * y
+            d = dOut[rows].double()
+            ww[rows, j] = (d * y).sum(1)
+            wx[rows] += w[rows, j, None].double() * (d @ V @ U)
+    for got, ref in ((out, want), (dX, wx), (dw, ww)):
+        assert float((got.double() - ref).norm() / ref.norm()) < 2.0 ** -8
+
+
+def test_captured_layer_replays_and_repeats(hq):
+    """The layer captured into a graph and replayed with new inputs, eager calls and
+    synchronizations between the replays, equals the eager result bit for bit each time."""
+    T, k, E, D, F = 100, 2, 6, 256, 384
+    q_up, _ = _quantized(hq, E * F, D, 4, 64, seed=1, exact=False)
+    q_down, _ = _quantized(hq, E * D, F, 4, 64, seed=2, exact=False)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def fresh(i):
+        return (torch.randn((T, D), device="cuda", generator=gen).half(),
+                torch.from_numpy(_ids(T, k, E, 0.1, i)).cuda(),
+                torch.rand((T, k), device="cuda", generator=gen),
+                torch.randn((T, D), device="cuda", generator=gen).half())
+    held = fresh(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _layer(hq, *held[:3], q_up, q_down, held[3])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _layer(hq, *held[:3], q_up, q_down, held[3])
+    for i in range(4):
+        new = fresh(i + 1)
+        for h, n in zip(held, new):
+            h.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = [g.clone() for g in got]
+        eager = _layer(hq, *new[:3], q_up, q_down, new[3])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(mine, eager))
+
+
+def test_calls_on_a_stream_of_their_own(hq):
+    q, W = _quantized(hq, 4 * 96, 256, 4, 64, seed=9)
+    s = torch.cuda.Stream()
+    X = _ints((50, 256), seed=1)
+    ids = torch.from_numpy(_ids(50, 2, 4, 0.1, 5)).cuda()
+    torch.cuda.synchronize()
+    r = hq.expert_sort(ids, 4, stream=s)
+    Y = hq.matmul_experts(X, q, r, out_f32=True, stream=s)
+    s.synchronize()
+    Xs = hq.expert_gather(X, r)
+    assert torch.equal(Y.double(), _want(Xs, W, r.offsets.cpu().numpy(), 96, False))
+
+
+def test_tensor_refusals(hq):
+    q, _ = _quantized(hq, 4 * 96, 256, 4, 64, seed=9)
+    r = hq.expert_sort(torch.zeros((5, 2), dtype=torch.int32, device="cuda"), 4)
+    X = torch.zeros((5, 256), dtype=torch.float16, device="cuda")
+    for bad in (X.float(), X[:4], X[:, :128], X.t(), X.cpu(), torch.zeros((5, 512), device="cuda").half()[:, ::2]):
+        with pytest.raises(ValueError):
+            hq.matmul_experts(bad, q, r)
+    with pytest.raises(ValueError):
+        hq.matmul_experts(X, q, r, sorted_rows=True)  # holds tokens, not sorted rows
+    with pytest.raises(ValueError):
+        hq.matmul_backward(torch.zeros((5, 4 * 96 - 1), device="cuda").half(), q)
+    wide, _ = _quantized(hq, 2000, 128, 4, 64, seed=9)
+    assert hq.hqq_matmul_backward_workspace_bytes(5, 2000, 128) > 16
+    with pytest.raises(ValueError):
+        hq.matmul_backward(torch.zeros((5, 2000), device="cuda").half(), wide,
+                           workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        hq.expert_combine(torch.zeros((10, 8), device="cuda"), r, torch.zeros(9, device="cuda"))
+    with pytest.raises(ValueError):
+        hq.expert_combine_backward(torch.zeros((5, 8), device="cuda"), torch.zeros((9, 8), device="cuda"),
+                                   r, torch.zeros((5, 2), device="cuda"))
+    with pytest.raises(ValueError):
+        hq.expert_gather(X, r, out=torch.empty((10, 255), dtype=torch.float16, device="cuda"))
+    with pytest.raises(hq.HQQError):
+        hq.expert_sort(torch.zeros((5, 2), dtype=torch.int32, device="cuda"), 2000)
