@@ -44,7 +44,9 @@ EXPORTED_SYMBOLS = ("hqq_quantize", "hqq_quantize_ex", "hqq_quantize_batch", "hq
                     "hqq_expert_combine", "hqq_expert_combine_backward", "hqq_matmul_experts",
                     "hqq_matmul_experts_backward", "hqq_matmul_experts_backward_workspace_bytes",
                     "hqq_adapters", "hqq_adapters_workspace_bytes", "hqq_adapters_backward",
-                    "hqq_adapters_backward_workspace_bytes")
+                    "hqq_adapters_backward_workspace_bytes",
+                    "hqq_matmul_adapters", "hqq_matmul_adapters_workspace_bytes",
+                    "hqq_matmul_adapters_backward", "hqq_matmul_adapters_backward_workspace_bytes")
 
 
 class HQQError(RuntimeError):
@@ -127,7 +129,10 @@ def load_library(path: str = LIB_PATH):
             ("hqq_matmul_experts_backward", [P, I64, I64, P, I, P, P, P, I64, I, I, P, I, P, P]),
             ("hqq_adapters", [P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P]),
             ("hqq_adapters_backward", [P, P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P, P,
-                                       P])):
+                                       P]),
+            ("hqq_matmul_adapters", [P, I64, I64, P, P, P, I64, I, I, P, P, I, I, P, P, P, I, P, P]),
+            ("hqq_matmul_adapters_backward", [P, P, I64, I64, P, P, P, I64, I, I, P, P, I, I, P, P, P,
+                                              I, P, P, P, P])):
         getattr(lib, name).restype = I
         getattr(lib, name).argtypes = args
     for name, args in (
@@ -135,7 +140,9 @@ def load_library(path: str = LIB_PATH):
             ("hqq_expert_sort_workspace_bytes", [I64, I, I]),
             ("hqq_matmul_experts_backward_workspace_bytes", [I64, I64, I64, I]),
             ("hqq_adapters_workspace_bytes", [I64, I64, I64, I, I]),
-            ("hqq_adapters_backward_workspace_bytes", [I64, I64, I64, I, I])):
+            ("hqq_adapters_backward_workspace_bytes", [I64, I64, I64, I, I]),
+            ("hqq_matmul_adapters_workspace_bytes", [I64, I64, I64, I, I, I, I]),
+            ("hqq_matmul_adapters_backward_workspace_bytes", [I64, I64, I64, I, I, I, I])):
         getattr(lib, name).restype = I64
         getattr(lib, name).argtypes = args
     lib.hqq_dequantize.restype = I
@@ -367,6 +374,37 @@ def hqq_adapters_backward(dY: int, X: int, dtype: int, M: int, K: int, A: int, B
 
 def hqq_adapters_backward_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
     return load_library().hqq_adapters_backward_workspace_bytes(M, N, K, rank, adapters)
+
+
+def hqq_matmul_adapters(X_f16: int, M: int, K: int, packed_codes: int, scale_f16: int,
+                        zero_f16: int, N: int, nbits: int, group_size: int, A_f16: int, B_f16: int,
+                        rank: int, adapters: int, ids_i32: int, scales_f32: int, Y: int,
+                        out_f32: int, workspace: int, stream: int = 0) -> int:
+    return load_library().hqq_matmul_adapters(X_f16, M, K, packed_codes, scale_f16, zero_f16, N,
+                                              nbits, group_size, A_f16, B_f16, rank, adapters,
+                                              ids_i32, scales_f32, Y, out_f32, workspace, stream)
+
+
+def hqq_matmul_adapters_workspace_bytes(M: int, N: int, K: int, nbits: int, group_size: int,
+                                        rank: int, adapters: int) -> int:
+    return load_library().hqq_matmul_adapters_workspace_bytes(M, N, K, nbits, group_size, rank,
+                                                              adapters)
+
+
+def hqq_matmul_adapters_backward(dY_f16: int, X_f16: int, M: int, K: int, packed_codes: int,
+                                 scale_f16: int, zero_f16: int, N: int, nbits: int,
+                                 group_size: int, A_f16: int, B_f16: int, rank: int, adapters: int,
+                                 ids_i32: int, scales_f32: int, dX: int, out_f32: int, dA_f32: int,
+                                 dB_f32: int, workspace: int, stream: int = 0) -> int:
+    return load_library().hqq_matmul_adapters_backward(
+        dY_f16, X_f16, M, K, packed_codes, scale_f16, zero_f16, N, nbits, group_size, A_f16, B_f16,
+        rank, adapters, ids_i32, scales_f32, dX, out_f32, dA_f32, dB_f32, workspace, stream)
+
+
+def hqq_matmul_adapters_backward_workspace_bytes(M: int, N: int, K: int, nbits: int,
+                                                 group_size: int, rank: int, adapters: int) -> int:
+    return load_library().hqq_matmul_adapters_backward_workspace_bytes(M, N, K, nbits, group_size,
+                                                                       rank, adapters)
 
 
 # ----------------------------------------------------------- torch helpers --
@@ -811,6 +849,14 @@ class ExpertOrder:
         return self.tokens * self.topk
 
 
+def _raw_stream(index: int) -> int:
+    """Handle of the device's current stream.  torch's raw getter where it has one: building a
+    Stream object for it takes 3 us, as long as a kernel launch."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(device, stream, call):
     """``call(stream handle)`` with ``device`` current and allocations tied to the stream."""
     import torch
@@ -820,9 +866,9 @@ def _launch(device, stream, call):
         with torch.cuda.stream(stream):
             return call(int(stream.cuda_stream))
     if device.index == torch.cuda.current_device():
-        return call(int(torch.cuda.current_stream().cuda_stream))
+        return call(_raw_stream(device.index))
     with torch.cuda.device(device):
-        return call(int(torch.cuda.current_stream().cuda_stream))
+        return call(_raw_stream(device.index))
 
 
 def _take(t, name: str, dtype, shape, device):
@@ -1112,17 +1158,58 @@ def adapters_backward(dY, X, A, B, ids, scales, base=None, out_f32: bool = False
     return _launch(dev, stream, call)
 
 
+def _projection(X, q: "QuantizedWeight", A, B, ids, scales):
+    """Checks a projection with adapters; returns the sizes of :func:`_adapter_shapes`."""
+    import torch
+    _, M, K, N, rank, n = _adapter_shapes(X, A, B, ids, scales)
+    _take(X, "X", torch.float16, (M, q.cols), X.device)
+    if N != q.rows:
+        raise ValueError(f"B has {N} outputs, the weight {q.rows}")
+    _weight_on(q, X.device)
+    return M, K, N, rank, n
+
+
 def matmul_adapters(X, q: "QuantizedWeight", A, B, ids, scales, out_f32: bool = False, out=None,
-                    stream=None):
-    """X Q^-1(W_q)^T plus every row's adapter: :func:`matmul` in float32, then :func:`adapters`
-    (float16 X; the sum is rounded once)."""
-    base = matmul(X, q, out_f32=True, stream=stream)
-    return adapters(X, A, B, ids, scales, base=base, out_f32=out_f32, out=out, stream=stream)
+                    workspace=None, stream=None):
+    """X Q^-1(W_q)^T plus every row's adapter (hqq_matmul_adapters): M x N float16 (or float32),
+    rounded once.  Arguments as for :func:`matmul` and :func:`adapters`, float16."""
+    import torch
+    M, K, N, rank, n = _projection(X, q, A, B, ids, scales)
+    dev = X.device
+    wb = _need(hqq_matmul_adapters_workspace_bytes(M, N, K, q.nbits, q.group_size, rank, n),
+               "hqq_matmul_adapters")
+
+    def call(sh):
+        y = _result(out, (M, N), torch.float32 if out_f32 else torch.float16, dev)
+        ws = _scratch(workspace, wb, dev)
+        _check_status(hqq_matmul_adapters(
+            _addr(X), M, K, _addr(q.packed), _addr(q.scale), _addr(q.zero), N, q.nbits,
+            q.group_size, _addr(A), _addr(B), rank, n, _addr(ids), _addr(scales), _addr(y),
+            int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_adapters")
+        return y
+    return _launch(dev, stream, call)
 
 
 def matmul_adapters_backward(dY, X, q: "QuantizedWeight", A, B, ids, scales, out_f32: bool = False,
-                             out=None, stream=None):
-    """The gradients of :func:`matmul_adapters` for a frozen weight: (dX, dA, dB)."""
-    base = matmul_backward(dY, q, out_f32=True, stream=stream)
-    return adapters_backward(dY, X, A, B, ids, scales, base=base, out_f32=out_f32, out=out,
-                             stream=stream)
+                             out=None, workspace=None, stream=None):
+    """The gradients of :func:`matmul_adapters` for a frozen weight
+    (hqq_matmul_adapters_backward): (dX, dA, dB), dX float16 (or float32), dA and dB float32."""
+    import torch
+    M, K, N, rank, n = _projection(X, q, A, B, ids, scales)
+    dev = X.device
+    _take(dY, "dY", torch.float16, (M, N), dev)
+    wb = _need(hqq_matmul_adapters_backward_workspace_bytes(M, N, K, q.nbits, q.group_size, rank,
+                                                            n), "hqq_matmul_adapters_backward")
+
+    def call(sh):
+        dX = _result(out, (M, K), torch.float32 if out_f32 else torch.float16, dev)
+        dA = torch.empty((n, rank, K), dtype=torch.float32, device=dev)
+        dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, wb, dev)
+        _check_status(hqq_matmul_adapters_backward(
+            _addr(dY), _addr(X), M, K, _addr(q.packed), _addr(q.scale), _addr(q.zero), N, q.nbits,
+            q.group_size, _addr(A), _addr(B), rank, n, _addr(ids), _addr(scales), _addr(dX),
+            int(bool(out_f32)), _addr(dA), _addr(dB), _addr(ws), sh),
+            "hqq_matmul_adapters_backward")
+        return dX, dA, dB
+    return _launch(dev, stream, call)

@@ -17,13 +17,15 @@ LIB = os.path.join(PKG, "libhqq_mi355x.so")
 SOURCES = [os.path.join(CSRC, "hqq_kernels.hip"), os.path.join(CSRC, "hqq_tensor_stop.hip"),
            os.path.join(CSRC, "hqq_matmul.hip"), os.path.join(CSRC, "hqq_experts.hip"),
            os.path.join(CSRC, "hqq_matmul_t.hip"), os.path.join(CSRC, "hqq_adapters.hip"),
-           os.path.join(CSRC, "hqq_route.hip"), os.path.join(CSRC, "hqq_lowrank.hip"),
+           os.path.join(CSRC, "hqq_route.hip"), os.path.join(CSRC, "hqq_group_gemm.hip"),
+           os.path.join(CSRC, "hqq_lowrank.hip"),
            os.path.join(CSRC, "hqq_meta.hip"), os.path.join(CSRC, "hqq_api.hip")]
 HEADERS = [os.path.join(CSRC, "hqq_internal.h"), os.path.join(CSRC, "hqq_solver.h"),
            os.path.join(CSRC, "hqq_tensor_stop.h"), os.path.join(CSRC, "hqq_matmul.h"),
            os.path.join(CSRC, "hqq_matmul_kernels.h"), os.path.join(CSRC, "hqq_codes.h"),
            os.path.join(CSRC, "hqq_tiles.h"), os.path.join(CSRC, "hqq_matmul_t.h"),
-           os.path.join(CSRC, "hqq_adapters.h"), os.path.join(CSRC, "hqq_route.h"),
+           os.path.join(CSRC, "hqq_adapters.h"), os.path.join(CSRC, "hqq_group_gemm.h"),
+           os.path.join(CSRC, "hqq_route.h"),
            os.path.join(CSRC, "hqq_lowrank.h"),
            os.path.join(ROOT, "include", "hqq.h")]
 

@@ -18,6 +18,8 @@ struct AdapterParams {
   const float* scales;      // adapters
   const void* base;         // M x N (backward: M x K), or null: zeros
   int base_f32;
+  int base_slabs;           // above 0: base is that many fp32 slabs, to be added in order
+  int64_t base_stride;      // floats of a slab
   void* out;                // Y: M x N (backward dX: M x K)
   int out_f32;
   const uint16_t* dY;       // backward: M x N
@@ -27,6 +29,14 @@ struct AdapterParams {
   int rank, adapters;
   void* workspace;
 };
+
+// A projection by a quantized weight with adapters, and its gradients: binary16 (dtype 0), base
+// null; `q` holds the weight (its X, Y and M are not read).
+struct MatmulParams;
+int64_t matmul_adapters_workspace_bytes(const MatmulParams& q, const AdapterParams& p);
+int64_t matmul_adapters_backward_workspace_bytes(const MatmulParams& q, const AdapterParams& p);
+hipError_t launch_matmul_adapters(MatmulParams q, AdapterParams p, int cus, hipStream_t stream);
+hipError_t launch_matmul_adapters_backward(const MatmulParams& q, AdapterParams p, hipStream_t stream);
 
 int64_t adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters);
 int64_t adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters);

@@ -17,7 +17,10 @@
 #include <stdint.h>
 
 #include "hqq_adapters.h"
+#include "hqq_group_gemm.h"
 #include "hqq_internal.h"
+#include "hqq_matmul.h"
+#include "hqq_matmul_t.h"
 #include "hqq_route.h"
 #include "hqq_tiles.h"
 
@@ -165,6 +168,12 @@ __global__ __launch_bounds__(kFewN) void hqq_adapter_expand_few_kernel(const Ada
 
 __device__ __forceinline__ float read_base(const AdapterParams& P, int64_t at) {
   if (!P.base) return 0.f;
+  if (P.base_slabs > 0) {
+    const float* b = static_cast<const float*>(P.base) + at;
+    float y = b[0];
+    for (int i = 1; i < P.base_slabs; ++i) y += b[i * P.base_stride];
+    return y;
+  }
   if (P.base_f32) return static_cast<const float*>(P.base)[at];
   const uint16_t v = static_cast<const uint16_t*>(P.base)[at];
   return P.dtype == 0 ? F16::up(v) : Bf16::up(v);
@@ -707,25 +716,26 @@ hipError_t launch_outer(const OuterParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+int few_splits(int64_t K) { return (int)((K + kFewK - 1) / kFewK); }
+
 template <typename D>
-hipError_t launch_few(const AdapterParams& p, hipStream_t st) {
-  const int splits = (int)((p.K + kFewK - 1) / kFewK);
-  float* part = static_cast<float*>(p.workspace);
-  if (splits > 0) {
-    const dim3 grid((unsigned)splits, (unsigned)p.M, (unsigned)((p.rank + kFewRank - 1) / kFewRank));
-    hipLaunchKernelGGL((hqq_adapter_shrink_few_kernel<D>), grid, dim3(kBlock), 0, st, p, part);
-  }
-  const dim3 grid((unsigned)((p.N + kFewN - 1) / kFewN), (unsigned)p.M);
-  hipLaunchKernelGGL((hqq_adapter_expand_few_kernel<D>), grid, dim3(kFewN), 0, st, p, part, splits);
+hipError_t launch_shrink_few(const AdapterParams& p, float* part, hipStream_t st) {
+  const dim3 grid((unsigned)few_splits(p.K), (unsigned)p.M, (unsigned)((p.rank + kFewRank - 1) / kFewRank));
+  hipLaunchKernelGGL((hqq_adapter_shrink_few_kernel<D>), grid, dim3(kBlock), 0, st, p, part);
   return hipGetLastError();
 }
 
 template <typename D>
-hipError_t launch_forward(const AdapterParams& p, hipStream_t st) {
-  if (p.M <= kFewRows) return launch_few<D>(p, st);
-  Layout l{static_cast<char*>(p.workspace)};
-  const SortedPlan w(l, p.M, p.rank, p.adapters);
-  hipError_t e = launch_route_sort(p.ids, p.M, p.adapters, w.order, w.position, w.offsets, w.sort_ws, st);
+hipError_t launch_expand_few(const AdapterParams& p, const float* part, hipStream_t st) {
+  const dim3 grid((unsigned)((p.N + kFewN - 1) / kFewN), (unsigned)p.M);
+  hipLaunchKernelGGL((hqq_adapter_expand_few_kernel<D>), grid, dim3(kFewN), 0, st, p, part, few_splits(p.K));
+  return hipGetLastError();
+}
+
+// Sort and first step of the sorted path.
+template <typename D>
+hipError_t launch_sorted_shrink(const AdapterParams& p, const SortedPlan& w, hipStream_t st) {
+  const hipError_t e = launch_route_sort(p.ids, p.M, p.adapters, w.order, w.position, w.offsets, w.sort_ws, st);
   if (e != hipSuccess) return e;
   ShrinkParams s = {};
   s.side[0] = {p.X, p.A, p.K, p.K, w.v, nullptr};
@@ -734,7 +744,19 @@ hipError_t launch_forward(const AdapterParams& p, hipStream_t st) {
   s.M = p.M;
   s.rank = p.rank;
   s.adapters = p.adapters;
-  e = launch_shrink<D>(s, 1, st);
+  return launch_shrink<D>(s, 1, st);
+}
+
+template <typename D>
+hipError_t launch_forward(const AdapterParams& p, hipStream_t st) {
+  if (p.M <= kFewRows) {
+    float* part = static_cast<float*>(p.workspace);
+    const hipError_t e = launch_shrink_few<D>(p, part, st);
+    return e != hipSuccess ? e : launch_expand_few<D>(p, part, st);
+  }
+  Layout l{static_cast<char*>(p.workspace)};
+  const SortedPlan w(l, p.M, p.rank, p.adapters);
+  const hipError_t e = launch_sorted_shrink<D>(p, w, st);
   if (e != hipSuccess) return e;
   return launch_expand<D>({w.v, p.B, p.scales, w.order, w.offsets, p.base, p.out, p.M, p.N, p.rank,
                            p.adapters, p.base_f32, p.out_f32}, st);
@@ -795,7 +817,7 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
 }  // namespace
 
 int64_t adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters) {
-  if (M <= kFewRows) return up256((K + kFewK - 1) / kFewK * M * rank * (int64_t)sizeof(float));
+  if (M <= kFewRows) return up256(few_splits(K) * M * rank * (int64_t)sizeof(float));
   Layout l{nullptr};
   const SortedPlan w(l, M, rank, adapters);
   return l.used;
@@ -813,6 +835,106 @@ hipError_t launch_adapters(const AdapterParams& p, hipStream_t stream) {
 
 hipError_t launch_adapters_backward(const AdapterParams& p, hipStream_t stream) {
   return p.dtype == 0 ? launch_backward<F16>(p, stream) : launch_backward<Bf16>(p, stream);
+}
+
+// The workspace of a projection with adapters: the adapters' own, then the base in fp32 and the
+// product's workspace (few rows), or the base in fp32 and its workspace (backward).
+int64_t matmul_adapters_workspace_bytes(const MatmulParams& q, const AdapterParams& p) {
+  const int64_t own = adapters_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters);
+  if (p.M > kFewRows) return own;
+  return own + up256(p.M * p.N * (int64_t)sizeof(float)) +
+         up256(matmul_workspace_bytes(p.M, p.N, p.K, q.nbits, q.group_size));
+}
+
+hipError_t launch_matmul_adapters(MatmulParams q, AdapterParams p, int cus, hipStream_t st) {
+  q.X = p.X;
+  q.M = p.M;
+  if (p.M > kFewRows) {
+    Layout l{static_cast<char*>(p.workspace)};
+    const SortedPlan w(l, p.M, p.rank, p.adapters);
+    const hipError_t e = launch_sorted_shrink<F16>(p, w, st);
+    if (e != hipSuccess) return e;
+    GroupGemmParams g = {};
+    g.X = p.X;
+    g.packed = q.packed;
+    g.scale16 = q.scale16;
+    g.zero16 = q.zero16;
+    g.Y = p.out;
+    g.M = p.M;
+    g.N = p.N;
+    g.K = p.K;
+    g.nbits = q.nbits;
+    g.group_shift = q.group_shift;
+    g.out_f32 = p.out_f32;
+    g.offsets = w.offsets;
+    g.order = w.order;
+    g.groups = p.adapters;
+    g.topk = 1;
+    g.low = w.v;
+    g.factor = p.B;
+    g.scales = p.scales;
+    g.rank = p.rank;
+    return launch_group_gemm(g, st);
+  }
+  Layout l{static_cast<char*>(p.workspace)};
+  float* part = l.take<float>(few_splits(p.K) * p.M * p.rank);
+  float* base = l.take<float>(p.M * p.N);
+  hipError_t e = launch_shrink_few<F16>(p, part, st);
+  if (e != hipSuccess) return e;
+  if (matmul_adds_low(q)) {
+    q.Y = p.out;
+    q.out_f32 = p.out_f32;
+    q.low = part;
+    q.low_splits = few_splits(p.K);
+    q.rank = p.rank;
+    q.adapters = p.adapters;
+    q.factor = p.B;
+    q.ids = p.ids;
+    q.scales = p.scales;
+    return launch_matmul(q, cus, st);
+  }
+  q.Y = base;
+  q.part = l.take<float>(0);
+  MatmulBase b;
+  e = launch_matmul_base(q, cus, &b, st);
+  if (e != hipSuccess) return e;
+  p.base = b.slabs > 0 ? q.part : base;
+  p.base_f32 = 1;
+  p.base_slabs = b.slabs;
+  p.base_stride = b.stride;
+  return launch_expand_few<F16>(p, part, st);
+}
+
+int64_t matmul_adapters_backward_workspace_bytes(const MatmulParams& q, const AdapterParams& p) {
+  return adapters_backward_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters) +
+         up256(p.M * p.K * (int64_t)sizeof(float)) + up256(matmul_t_workspace_bytes(p.M, p.N, p.K, 0));
+}
+
+hipError_t launch_matmul_adapters_backward(const MatmulParams& q, AdapterParams p, hipStream_t st) {
+  Layout l{static_cast<char*>(p.workspace) + adapters_backward_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters)};
+  float* base = l.take<float>(p.M * p.K);
+  if (p.M > 0) {
+    MatmulTParams t = {};
+    t.dY = p.dY;
+    t.packed = q.packed;
+    t.scale16 = q.scale16;
+    t.zero16 = q.zero16;
+    t.dX = base;
+    t.M = p.M;
+    t.N = p.N;
+    t.K = p.K;
+    t.nbits = q.nbits;
+    t.group_size = q.group_size;
+    t.group_shift = q.group_shift;
+    t.out_f32 = 1;
+    t.part = l.take<float>(0);
+    t.nsplit = 1;
+    const hipError_t e = launch_matmul_t(t, st);
+    if (e != hipSuccess) return e;
+    p.base = base;
+    p.base_f32 = 1;
+  }
+  return launch_adapters_backward(p, st);
 }
 
 }  // namespace hqq

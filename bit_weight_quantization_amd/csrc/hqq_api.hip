@@ -599,6 +599,7 @@ namespace {
 
 constexpr int64_t kMaxGroupedRows = 8000000;  // row tiles of the grid's second dimension
 constexpr int64_t kMaxAdapterRows = 4000000;
+constexpr int64_t kMaxInner = 1 << 24;        // K: 64 weight rows stay within 32-bit offsets
 
 int group_shift_of(int group_size) {
   return group_size == 16 ? 4 : group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
@@ -612,7 +613,7 @@ int validate_product(int64_t M, int64_t N, int64_t K, int experts, int nbits, in
   if (!supported_nbits(nbits) || !supported_group(group_size)) return HQQ_ERR_UNSUPPORTED;
   if (K % group_size != 0) return HQQ_ERR_INVALID_ARG;
   if (K % 32 != 0) return HQQ_ERR_UNSUPPORTED;
-  return M > kMaxGroupedRows ? HQQ_ERR_INVALID_ARG : HQQ_OK;
+  return M > kMaxGroupedRows || K > kMaxInner ? HQQ_ERR_INVALID_ARG : HQQ_OK;
 }
 
 int validate_experts(int experts) {
@@ -912,6 +913,117 @@ int hqq_adapters_backward(const void* dY, const void* X, int dtype, int64_t M, i
   p.adapters = adapters;
   p.workspace = workspace;
   return hqq::launch_adapters_backward(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+// The weight and the sizes of a projection with adapters.
+static int projection_params(int64_t M, int64_t N, int64_t K, const void* packed, const void* scale,
+                             const void* zero, int nbits, int group_size, int rank, int adapters,
+                             hqq::MatmulParams* q, hqq::AdapterParams* p) {
+  int st = validate_product(M, N, K, 0, nbits, group_size);
+  if (st == HQQ_OK) st = validate_adapters(HQQ_DTYPE_F16, M, N, K, rank, adapters);
+  if (st != HQQ_OK) return st;
+  *p = {};
+  q->packed = static_cast<const uint8_t*>(packed);
+  q->scale16 = static_cast<const uint16_t*>(scale);
+  q->zero16 = static_cast<const uint16_t*>(zero);
+  q->M = p->M = M;
+  q->N = p->N = N;
+  q->K = p->K = K;
+  q->nbits = nbits;
+  q->group_size = group_size;
+  q->group_shift = group_shift_of(group_size);
+  q->part = nullptr;
+  q->slab = 0;
+  q->ksplit = 1;
+  p->dtype = HQQ_DTYPE_F16;
+  p->rank = rank;
+  p->adapters = adapters;
+  return HQQ_OK;
+}
+
+int64_t hqq_matmul_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits,
+                                            int group_size, int rank, int adapters) {
+  hqq::MatmulParams q = {};
+  hqq::AdapterParams p;
+  if (projection_params(M, N, K, nullptr, nullptr, nullptr, nbits, group_size, rank, adapters, &q, &p) != HQQ_OK)
+    return -1;
+  return hqq::matmul_adapters_workspace_bytes(q, p);
+}
+
+int64_t hqq_matmul_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits,
+                                                     int group_size, int rank, int adapters) {
+  hqq::MatmulParams q = {};
+  hqq::AdapterParams p;
+  if (projection_params(M, N, K, nullptr, nullptr, nullptr, nbits, group_size, rank, adapters, &q, &p) != HQQ_OK)
+    return -1;
+  return hqq::matmul_adapters_backward_workspace_bytes(q, p);
+}
+
+int hqq_matmul_adapters(const void* X_f16, int64_t M, int64_t K, const void* packed_codes,
+                        const void* scale_f16, const void* zero_f16, int64_t N, int nbits,
+                        int group_size, const void* A_f16, const void* B_f16, int rank, int adapters,
+                        const void* ids_i32, const void* scales_f32, void* Y, int out_f32,
+                        void* workspace, void* stream) {
+  hqq::MatmulParams q = {};
+  hqq::AdapterParams p;
+  const int st = projection_params(M, N, K, packed_codes, scale_f16, zero_f16, nbits, group_size, rank, adapters, &q, &p);
+  if (st != HQQ_OK) return st;
+  if (out_f32 != 0 && out_f32 != 1) return HQQ_ERR_INVALID_ARG;
+  if (M == 0) return HQQ_OK;
+  if (!X_f16 || !packed_codes || !scale_f16 || !zero_f16 || !A_f16 || !B_f16 || !ids_i32 ||
+      !scales_f32 || !Y || !workspace)
+    return HQQ_ERR_INVALID_ARG;
+  if (!aligned(X_f16, 16) || !aligned(packed_codes, 16) || !aligned(scale_f16, 2) ||
+      !aligned(zero_f16, 2) || !aligned(A_f16, 16) || !aligned(B_f16, 16) || !aligned(ids_i32, 4) ||
+      !aligned(scales_f32, 4) || !aligned(Y, out_f32 ? 4 : 2) || !aligned(workspace, 256))
+    return HQQ_ERR_ALIGNMENT;
+  p.X = static_cast<const uint16_t*>(X_f16);
+  p.A = static_cast<const uint16_t*>(A_f16);
+  p.B = static_cast<const uint16_t*>(B_f16);
+  p.ids = static_cast<const int32_t*>(ids_i32);
+  p.scales = static_cast<const float*>(scales_f32);
+  p.out = Y;
+  p.out_f32 = out_f32;
+  p.workspace = workspace;
+  const int cus = compute_units();
+  if (cus <= 0) return HQQ_ERR_LAUNCH;
+  const hipError_t err = hqq::launch_matmul_adapters(q, p, cus, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int hqq_matmul_adapters_backward(const void* dY_f16, const void* X_f16, int64_t M, int64_t K,
+                                 const void* packed_codes, const void* scale_f16,
+                                 const void* zero_f16, int64_t N, int nbits, int group_size,
+                                 const void* A_f16, const void* B_f16, int rank, int adapters,
+                                 const void* ids_i32, const void* scales_f32, void* dX, int out_f32,
+                                 void* dA_f32, void* dB_f32, void* workspace, void* stream) {
+  hqq::MatmulParams q = {};
+  hqq::AdapterParams p;
+  const int st = projection_params(M, N, K, packed_codes, scale_f16, zero_f16, nbits, group_size, rank, adapters, &q, &p);
+  if (st != HQQ_OK) return st;
+  if (out_f32 != 0 && out_f32 != 1) return HQQ_ERR_INVALID_ARG;
+  if (!dA_f32 || !dB_f32 || !workspace) return HQQ_ERR_INVALID_ARG;
+  if (M > 0 && (!dY_f16 || !X_f16 || !packed_codes || !scale_f16 || !zero_f16 || !A_f16 || !B_f16 ||
+                !ids_i32 || !scales_f32 || !dX))
+    return HQQ_ERR_INVALID_ARG;
+  if (!aligned(dY_f16, 2) || !aligned(X_f16, 16) || !aligned(packed_codes, 16) ||
+      !aligned(scale_f16, 2) || !aligned(zero_f16, 2) || !aligned(A_f16, 16) || !aligned(B_f16, 16) ||
+      !aligned(ids_i32, 4) || !aligned(scales_f32, 4) || !aligned(dX, out_f32 ? 4 : 2) ||
+      !aligned(dA_f32, 16) || !aligned(dB_f32, 16) || !aligned(workspace, 256))
+    return HQQ_ERR_ALIGNMENT;
+  p.dY = static_cast<const uint16_t*>(dY_f16);
+  p.X = static_cast<const uint16_t*>(X_f16);
+  p.A = static_cast<const uint16_t*>(A_f16);
+  p.B = static_cast<const uint16_t*>(B_f16);
+  p.ids = static_cast<const int32_t*>(ids_i32);
+  p.scales = static_cast<const float*>(scales_f32);
+  p.out = dX;
+  p.out_f32 = out_f32;
+  p.dA = static_cast<float*>(dA_f32);
+  p.dB = static_cast<float*>(dB_f32);
+  p.workspace = workspace;
+  const hipError_t err = hqq::launch_matmul_adapters_backward(q, p, static_cast<hipStream_t>(stream));
+  return err == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "hqq_group_gemm.h"
 #include "hqq_internal.h"
 #include "hqq_matmul.h"
 #include "hqq_matmul_kernels.h"
@@ -48,10 +49,24 @@ void launch_skinny(const MatmulParams& P, hipStream_t st) {
   else launch_skinny_nw<NB, MT, 1>(P, st);
 }
 
-template <int NB, int WM>
-void launch_gemm(const MatmulParams& P, hipStream_t st) {
-  const dim3 grid((unsigned)((P.N + 127) / 128), (unsigned)max_row_tiles(P.M, P.experts, 64 * WM));
-  hipLaunchKernelGGL((hqq_gemm_kernel<NB, WM, 2, 2, true>), grid, dim3(2 * WM * kWave), 0, st, P);
+hipError_t launch_tiles(const MatmulParams& P, hipStream_t st) {
+  GroupGemmParams g = {};
+  g.X = P.X;
+  g.packed = P.packed;
+  g.scale16 = P.scale16;
+  g.zero16 = P.zero16;
+  g.Y = P.Y;
+  g.M = P.M;
+  g.N = P.N;
+  g.K = P.K;
+  g.nbits = P.nbits;
+  g.group_shift = P.group_shift;
+  g.out_f32 = P.out_f32;
+  g.offsets = P.offsets;
+  g.order = P.order;
+  g.groups = P.experts;
+  g.topk = P.topk;
+  return launch_group_gemm(g, st);
 }
 
 template <int NB>
@@ -70,8 +85,7 @@ hipError_t launch_nb(const MatmulParams& P, hipStream_t st) {
   if (mean <= 8) launch_skinny<NB, 1>(P, st);
   else if (mean <= 24) launch_skinny<NB, 2>(P, st);
   else if (mean <= 48) launch_skinny<NB, 4>(P, st);
-  else if (mean <= 256) launch_gemm<NB, 2>(P, st);
-  else launch_gemm<NB, 4>(P, st);
+  else return launch_tiles(P, st);
   return hipGetLastError();
 }
 

@@ -1,0 +1,32 @@
+// hqq_group_gemm.h -- launch interface of the tiled products of sorted rows with quantized
+// weights (hqq_group_gemm.hip).  Not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hqq {
+
+struct GroupGemmParams {
+  const uint16_t* X;        // binary16 rows of K, 16-byte aligned
+  const uint8_t* packed;
+  const uint16_t* scale16;
+  const uint16_t* zero16;
+  void* Y;                  // rows of N, binary16 or fp32
+  int64_t M, N, K;          // M sorted rows
+  int nbits, group_shift;
+  int out_f32;
+  const int32_t* offsets;   // first sorted row of every group, groups + 1 values
+  const int32_t* order;     // experts: null, or row i is X[order[i] / topk]; adapters: row of X and Y
+  int groups, topk;
+  // adapters (low != null): every group multiplies with the one weight, and adds
+  // scales[g] low[i] factor[g]^T
+  const float* low;         // M x rank, sorted
+  const uint16_t* factor;   // groups x N x rank
+  const float* scales;
+  int rank;
+};
+
+// experts x N x K weights (p.low null), or one weight and adapters.
+hipError_t launch_group_gemm(const GroupGemmParams& p, hipStream_t stream);
+
+}  // namespace hqq

@@ -1,0 +1,448 @@
+// hqq_group_gemm.hip -- gfx950 kernels of the tiled products of sorted rows with quantized
+// weights, Y[i] = X[i] Q^-1(W)^T: with every expert's own weight, or with one weight and every
+// adapter's low-rank product added to the same accumulators.
+//
+// A block's four wavefronts share 32 TI rows of X through LDS, and each takes 32 TJ weight rows
+// of its own: it decodes its codes straight into the matrix operand (no LDS for the weight, and
+// no weight is decoded twice in a block), so an LDS read feeds TJ matrix instructions.  The
+// tiles of the shared-weight kernel, 64 x 64 per wavefront with both operands in LDS, read as
+// many LDS bytes per cycle as the CU can give before its matrix cores are busy.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "hqq_codes.h"
+#include "hqq_group_gemm.h"
+#include "hqq_internal.h"
+#include "hqq_tiles.h"
+
+namespace hqq {
+namespace {
+
+constexpr int kGK = 64;            // k per step
+constexpr int kGRow = kGK + 8;     // halves per LDS row of X (rows 4 banks apart)
+constexpr int kGWaves = 4;
+constexpr int kGTables = 4;        // ring of the scales' LDS tables, of 4 groups each
+
+constexpr float kSub = 16777216.f;  // 2^24: a binary16 subnormal's unit is 2^-24
+
+// s*q - s*z of two codes as binary16: fma in fp32 (s z exact, one rounding), rounded to binary16.
+// The codes come as the halves of t, each shifted left inside an otherwise empty half: read as
+// binary16 that is a subnormal, q 2^(shift - 24) exactly, and the scales carry the power back.  Two
+// instructions a pair, where conversion in fp32 and a packing conversion take three (and
+// exponents put in front of the codes one more).
+__device__ __forceinline__ uint32_t weight_pair(uint32_t t, float s_lo, float s_hi, float minus_sz) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, %4 op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixhi_f16 %0, %1, %3, %4 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+      : "=&v"(d) : "v"(t), "v"(s_lo), "v"(s_hi), "v"(minus_sz));
+  return d;
+}
+
+// A group's scales as decode_pair takes them: s 2^24 and -s z; the other shifts' powers of s.
+struct PairScale {
+  float a, c;
+};
+
+// Codes 8 step + 2 e and + 1 of a lane's 32 (LSB first in w) as two binary16 weights.
+template <int NB>
+__device__ __forceinline__ uint32_t decode_pair(const uint32_t (&w)[NB], int step, int e, PairScale p) {
+  if constexpr (NB == 3) {         // codes straddle bytes: one by one
+    const float sv = p.a * (1.f / kSub);
+    const float w0 = __builtin_fmaf(sv, (float)code_at<NB>(w, 8 * step + 2 * e), p.c);
+    const float w1 = __builtin_fmaf(sv, (float)code_at<NB>(w, 8 * step + 2 * e + 1), p.c);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t){w0, w1}, half2_t));
+  } else if constexpr (NB == 8) {  // bytes 2 e, 2 e + 1 of two words
+    const uint32_t t = __builtin_amdgcn_perm(0u, w[2 * step + (e >> 1)], (e & 1) ? 0x0C030C02u : 0x0C010C00u);
+    return weight_pair(t, p.a, p.a, p.c);
+  } else if constexpr (NB == 4) {  // byte e of a word, in both halves
+    const uint32_t t = __builtin_amdgcn_perm(0u, w[step], 0x0C000C00u | (uint32_t)e | ((uint32_t)e << 16));
+    return weight_pair(t & 0x00F0000Fu, p.a, p.a * (1.f / 16.f), p.c);
+  } else {                         // byte 2 (step % 2) + e / 2 of a word, two of its four codes
+    const uint32_t at = (uint32_t)(2 * (step & 1) + (e >> 1));
+    const uint32_t t = __builtin_amdgcn_perm(0u, w[step >> 1], 0x0C000C00u | at | (at << 16));
+    return e & 1 ? weight_pair(t & 0x00C00030u, p.a * (1.f / 16.f), p.a * (1.f / 64.f), p.c)
+                 : weight_pair(t & 0x000C0003u, p.a, p.a * (1.f / 4.f), p.c);
+  }
+}
+
+// Lane i + 32 h holds, per step of 64, the values 32 h .. + 32 of row i of both operands; the
+// four matrix steps (v_mfma_f32_32x32x16_f16) take 8 of them each, the instruction's k order
+// being the same for both.  The weight is the A operand and row 8 a + 4 h + b of tile j stands
+// for weight row 32 h + 16 j + 4 a + b (TJ = 2) of the wavefront's, so that a lane ends with 16 TJ
+// consecutive outputs of one row of X.  X goes through LDS one step ahead, double-buffered; codes
+// and X are loaded a step ahead in registers, two wavefronts per SIMD.
+template <int NB, int TI, int TJ, bool G16, bool ADAPTERS>
+__global__ __launch_bounds__(kGWaves * kWave) __attribute__((amdgpu_waves_per_eu(2)))
+void hqq_group_gemm_kernel(const GroupGemmParams P) {
+  constexpr int BM = 32 * TI;
+  constexpr int T = kGWaves * kWave;
+  constexpr int XP = BM * kGK / 8 / T;      // 16-byte pieces of X per thread and step
+  constexpr int XT = T / (kGK / 8);         // rows of X per round of loads
+  constexpr int RC = 64;                    // low-rank values per round (adapters)
+  static_assert(XP >= 1 && 4 * TJ % TI == 0, "a piece per thread at least, decoding in whole pairs");
+  constexpr int BN = 32 * TJ * kGWaves;     // weight rows: one per thread
+  static_assert(BN == T, "a thread loads the scales of one weight row");
+  __shared__ __align__(16) _Float16 As[2][BM][kGRow];
+  __shared__ PairScale Sz[kGTables][4][BN];  // s 2^24 and -s z of the block's rows
+  const int64_t cols = (P.N + BN - 1) / BN;
+  const TilePlace place = place_tile(blockIdx.x, count_row_tiles(P.offsets, P.groups, P.M, BM), cols);
+  if (place.tile < 0) return;
+  const RowTile t = find_row_tile(P.offsets, P.groups, P.M, BM, place.tile);
+  if (t.rows <= 0) return;
+  const int tid = threadIdx.x;
+  const int wid = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid & (kWave - 1);
+  const int i = lane & 31, h = lane >> 5;
+  const int64_t n0 = place.col * BN + wid * (32 * TJ);
+  const bool none = t.group == P.groups;
+  const int used = (t.rows + 31) >> 5;  // fragments of 32 rows that hold any
+  const int64_t w0 = ADAPTERS || none ? 0 : (int64_t)t.group * P.N;
+  const int K = !ADAPTERS && none ? 0 : (int)P.K;  // rows of no expert: zeros
+  const int64_t row_bytes = (P.K >> 3) * NB, gpr = P.K >> P.group_shift;
+
+  // rows past the tile read its last row; weight rows past N the last one (results not stored)
+  const int xp = tid & 7, xr = tid >> 3;
+  const uint16_t* xrow[XP];
+#pragma unroll
+  for (int p = 0; p < XP; ++p) {
+    const int m = xr + XT * p;
+    const int64_t row = t.row0 + (m < t.rows ? m : t.rows - 1);
+    int64_t src = row;
+    if constexpr (ADAPTERS) {
+      const int32_t o = P.order[row];
+      src = o < 0 ? ~o : o;
+    } else if (P.order) {
+      src = P.order[row] / P.topk;
+      if (src < 0) src = 0;  // (rows of no expert read nothing)
+    }
+    xrow[p] = P.X + src * P.K;
+  }
+  // the wavefront's first weight row, and the lane's rows as 32-bit offsets from it (64 rows of
+  // K <= 2^24 codes)
+  const int64_t wave_row = w0 + (n0 < P.N ? n0 : P.N - 1);
+  const uint8_t* wbase = P.packed + wave_row * row_bytes;
+  uint32_t woff[TJ];
+  int srow[TJ];  // the lane's rows in the scales' table
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const int r = 16 * TJ * ((i >> 2) & 1) + 16 * j + 4 * (i >> 3) + (i & 3);
+    srow[j] = wid * (32 * TJ) + r;
+    woff[j] = (uint32_t)(w0 + (n0 + r < P.N ? n0 + r : P.N - 1) - wave_row) * (uint32_t)row_bytes;
+  }
+  const int64_t trow = place.col * BN + tid;
+  const int64_t sfirst = (w0 + (trow < P.N ? trow : P.N - 1)) * gpr;
+  // The scales of 4 groups of a row are 8 contiguous bytes, loaded at once by the row's thread two
+  // tables ahead and put into LDS a step later.  (Loaded by the lanes that decode, step by step, each
+  // 2-byte load touched 32 lines and the address unit bound the kernel: 1147 instead of 601 us for
+  // 4096 rows, 8 experts of 11008 x 4096.)  The load stays inside the arrays: at their end it starts
+  // earlier and is shifted back.
+  const int tk = 4 << P.group_shift;  // k of a table
+  const int64_t sgroups = (ADAPTERS ? P.N : P.N * P.groups) * gpr;
+  uint64_t s4, z4;
+  auto load_scales = [&](int k0) {
+    const int64_t want = sfirst + (k0 < K ? k0 >> P.group_shift : 0);
+    if (sgroups >= 4) {  // uniform
+      const int64_t at = want < sgroups - 4 ? want : sgroups - 4;
+      __builtin_memcpy(&s4, P.scale16 + at, 8);
+      __builtin_memcpy(&z4, P.zero16 + at, 8);
+      const int shift = 16 * (int)(want - at);
+      s4 >>= shift;
+      z4 >>= shift;
+    } else {             // a weight of less than four groups in all
+      s4 = z4 = 0;
+      for (int e = 0; e < 4; ++e) {
+        const int64_t at = want + e < sgroups ? want + e : sgroups - 1;
+        s4 |= (uint64_t)P.scale16[at] << (16 * e);
+        z4 |= (uint64_t)P.zero16[at] << (16 * e);
+      }
+    }
+  };
+  auto write_scales = [&](int k0) {
+    const int table = (k0 >> (P.group_shift + 2)) & (kGTables - 1);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float f = h2f((uint32_t)(s4 >> (16 * c)) & 0xffffu);
+      Sz[table][c][tid] = {f * kSub, -f * h2f((uint32_t)(z4 >> (16 * c)) & 0xffffu)};
+    }
+  };
+
+  uint4 xv[XP];
+  struct Codes {
+    uint32_t w[TJ][NB];
+  };
+  auto load_x = [&](int k0) {
+    const int k = k0 + 8 * xp;
+#pragma unroll
+    for (int p = 0; p < XP; ++p) xv[p] = *reinterpret_cast<const uint4*>(xrow[p] + (k < K ? k : 0));
+  };
+  auto write_x = [&](int buf, int k0) {
+    if (k0 + kGK > K && k0 + 8 * xp >= K) {  // the last step's upper half
+#pragma unroll
+      for (int p = 0; p < XP; ++p) xv[p] = make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int p = 0; p < XP; ++p) *reinterpret_cast<uint4*>(&As[buf][xr + XT * p][8 * xp]) = xv[p];
+  };
+  auto load_codes = [&](int k0, Codes& c) {
+    const uint32_t kk = k0 + 32 * h < K ? k0 + 32 * h : 0;  // K is a multiple of 32
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) load_codes32<NB>(wbase + (uint64_t)(woff[j] + (kk >> 5) * (4 * NB)), c.w[j]);
+  };
+
+  float16_t acc[TI][TJ];
+#pragma unroll
+  for (int a = 0; a < TI; ++a)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[a][j][v] = 0.f;
+
+  // the lane's scales of the step at k0: of codes 0-15 and 16-31 (different groups only when g = 16)
+  struct Scales {
+    PairScale p[TJ][2];
+  };
+  auto read_scales = [&](int k0, Scales& o) {
+    const int g = (k0 + 32 * h) >> P.group_shift;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      o.p[j][0] = Sz[(g >> 2) & (kGTables - 1)][g & 3][srow[j]];
+      o.p[j][1] = G16 ? Sz[(g >> 2) & (kGTables - 1)][(g & 3) + 1][srow[j]] : o.p[j][0];
+    }
+    if (k0 + kGK > K && k0 + 32 * h >= K) {  // the last step's upper half: weights of zero
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) o.p[j][0] = o.p[j][1] = {0.f, 0.f};
+    }
+  };
+  uint32_t wf[2][TJ][4];  // decoded weights of a matrix step and of the next one
+  // One step: the loads of the next one first, then 4 matrix steps of TI slots each.  A slot is the
+  // products of one X fragment, the read of the fragment that takes its place one matrix step later
+  // (4 slots ahead: the products between cover the LDS latency) and a slice of the decoding of the
+  // next matrix step's weights (after the last one, of the next step's first); the scheduling
+  // barriers keep this order.
+  auto step = [&](int buf, int k0, const Codes& cur, Codes& nxt, const Scales& sc, Scales& sn) {
+    const int kn = k0 + kGK < K ? k0 + kGK : 0;  // (past the end: unused)
+    half8_t xf[TI];
+    auto read_x = [&](int s, int a) {
+      xf[a] = *reinterpret_cast<const half8_t*>(&As[buf][32 * a + i][32 * h + 8 * s]);
+    };
+#pragma unroll
+    for (int a = 0; a < TI; ++a)
+      if (a < used) read_x(0, a);
+    load_x(kn);
+    load_codes(kn, nxt);
+    const bool refill = (k0 & (tk - 1)) == 0;  // a new table began: load the one after the next
+    if (refill) load_scales(k0 + 2 * tk);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s == 2) read_scales(kn, sn);  // (its table was written a barrier ago at least)
+#pragma unroll
+      for (int a = 0; a < TI; ++a) {
+if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(half8_t, make_uint4(wf[s & 1][j][0], wf[s & 1][j][1], wf[s & 1][j][2], wf[s & 1][j][3])),
+                xf[a], acc[a][j], 0, 0, 0);
+          if (s < 3) read_x(s + 1, a);
+        }
+#pragma unroll
+        for (int q = a * (4 * TJ / TI); q < (a + 1) * (4 * TJ / TI); ++q) {
+          const int j = q % TJ, e = q / TJ;
+          wf[(s + 1) & 1][j][e] = s < 3 ? decode_pair<NB>(cur.w[j], s + 1, e, sc.p[j][(s + 1) >> 1])
+                                        : decode_pair<NB>(nxt.w[j], 0, e, sn.p[j][0]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    write_x(buf ^ 1, k0 + kGK);
+    if (refill) write_scales(k0 + 2 * tk);
+    lds_barrier();
+  };
+  if (K > 0) {
+    Codes ca, cb;
+    Scales sa, sb;
+    load_x(0);
+    load_codes(0, ca);
+    load_scales(0);
+    write_x(0, 0);
+    write_scales(0);
+    load_scales(tk);
+    write_scales(tk);
+    lds_barrier();
+    read_scales(0, sa);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) wf[0][j][e] = decode_pair<NB>(ca.w[j], 0, e, sa.p[j][0]);
+    int k0 = 0;
+    for (; k0 + kGK < K; k0 += 2 * kGK) {
+      step(0, k0, ca, cb, sa, sb);
+      step(1, k0 + kGK, cb, ca, sb, sa);
+    }
+    if (k0 < K) step(0, k0, ca, cb, sa, sb);
+  }
+
+  float back[TI];
+#pragma unroll
+  for (int a = 0; a < TI; ++a) back[a] = 1.f;
+  if constexpr (ADAPTERS) {
+    // The low-rank product joins the same accumulators: s low[m] enters as two binary16 parts of
+    // the row scaled by a power of two (22 bits below the row's largest value), the accumulators of
+    // the row are scaled alike (exact) and scaled back below.
+    if (!none) {
+      __shared__ float scale_up[BM];
+      _Float16* parts = &As[0][0][0];  // [2][BM][RC + 8]: as large as the X buffers
+      const float s = P.scales[t.group];
+      {
+        // 16-byte pieces of row xr + XT p at 4 xp, 4 xp + 32, ..; 8 threads share a row
+#pragma unroll
+        for (int p = 0; p < XP; ++p) {
+          const int m = xr + XT * p;
+          float largest = 0.f;
+          if (m < t.rows)
+            for (int r = xp; r < P.rank; r += 8) {
+              const float v = s * P.low[(t.row0 + m) * P.rank + r];
+              largest = __builtin_isfinite(v) ? __builtin_fmaxf(largest, __builtin_fabsf(v)) : largest;
+            }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) largest = __builtin_fmaxf(largest, __shfl_xor(largest, o, kWave));
+          // 2^x: the largest comes to [2^13, 2^14); within 2^-40 .. 2^40, so that the accumulators stay
+          // finite (smaller rows then lose what lies below 2^-64)
+          int x = 13 - ((int)((__builtin_bit_cast(uint32_t, largest) >> 23) & 255) - 127);
+          x = x > 40 ? 40 : x < -114 ? -114 : x;
+          if (xp == 0) scale_up[m] = __builtin_bit_cast(float, (uint32_t)(127 + x) << 23);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int a = 0; a < TI; ++a) {
+        const float up = scale_up[32 * a + i];
+        back[a] = __builtin_bit_cast(float, (uint32_t)(254 << 23) - __builtin_bit_cast(uint32_t, up));  // 1 / up
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[a][j][v] *= up;
+      }
+      for (int r0 = 0; r0 < P.rank; r0 += RC) {
+        // thread: rows xr + XT p, low-rank values 8 xp .. + 8 of the round
+#pragma unroll
+        for (int p = 0; p < XP; ++p) {
+          const int m = xr + XT * p, r = r0 + 8 * xp;
+          half8_t hi, lo;
+          const float up = s * scale_up[m];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = m < t.rows && r < P.rank ? up * P.low[(t.row0 + m) * P.rank + r + e] : 0.f;
+            hi[e] = (_Float16)v;
+            lo[e] = __builtin_isfinite((float)hi[e]) ? (_Float16)(v - (float)hi[e]) : (_Float16)0.f;
+          }
+          *reinterpret_cast<half8_t*>(parts + m * kGRow + 8 * xp) = hi;
+          *reinterpret_cast<half8_t*>(parts + (BM + m) * kGRow + 8 * xp) = lo;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int st = 0; st < RC / 16; ++st) {
+          const int r = r0 + 16 * st + 8 * h;
+          if (r0 + 16 * st >= P.rank) break;  // uniform
+          half8_t wf[TJ];
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) {
+            const int64_t n = n0 + 16 * TJ * ((i >> 2) & 1) + 16 * j + 4 * (i >> 3) + (i & 3);
+            wf[j] = (half8_t){};
+            if (n < P.N && r < P.rank)
+              wf[j] = *reinterpret_cast<const half8_t*>(P.factor + ((int64_t)t.group * P.N + n) * P.rank + r);
+          }
+#pragma unroll
+          for (int a = 0; a < TI; ++a) {
+            const _Float16* src = parts + (32 * a + i) * kGRow + 16 * st + 8 * h;
+            const half8_t hi = *reinterpret_cast<const half8_t*>(src);
+            const half8_t lo = *reinterpret_cast<const half8_t*>(src + BM * kGRow);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) {
+              acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[j], hi, acc[a][j], 0, 0, 0);
+              acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[j], lo, acc[a][j], 0, 0, 0);
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+  }
+
+  // lane: row 32 a + i of the tile, outputs n0 + 16 TJ h .. + 16 TJ (element 4 a' + b of tile j:
+  // register 4 a' + b)
+  const int64_t n = n0 + 16 * TJ * h;
+#pragma unroll
+  for (int a = 0; a < TI; ++a) {
+    const int m = 32 * a + i;
+    if (m >= t.rows || n >= P.N) continue;
+    int64_t row = t.row0 + m;
+    if constexpr (ADAPTERS) {
+      const int32_t o = P.order[row];
+      row = o < 0 ? ~o : o;
+    }
+    const int64_t at = row * P.N + n, left = P.N - n;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      if (P.out_f32) {
+        float* y = static_cast<float*>(P.Y) + at + 16 * j;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = back[a] * acc[a][j][e];
+        if (left >= 16 * (j + 1)) {
+          __builtin_memcpy(y, v, 64);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (16 * j + e < left) y[e] = v[e];
+        }
+      } else {
+        _Float16* y = static_cast<_Float16*>(P.Y) + at + 16 * j;
+        _Float16 v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = (_Float16)(back[a] * acc[a][j][e]);
+        if (left >= 16 * (j + 1)) {
+          __builtin_memcpy(y, v, 32);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (16 * j + e < left) y[e] = v[e];
+        }
+      }
+    }
+  }
+}
+
+template <int NB, int TI, bool ADAPTERS>
+hipError_t launch_tile(const GroupGemmParams& p, hipStream_t st) {
+  constexpr int kCols = kGWaves * 64;
+  const int64_t blocks = (p.N + kCols - 1) / kCols * max_row_tiles(p.M, p.groups, 32 * TI);
+  const dim3 grid((unsigned)((blocks + 7) & ~(int64_t)7));  // (every XCD its share)
+  const dim3 block(kGWaves * kWave);
+  if (p.group_shift == 4) hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, true, ADAPTERS>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, false, ADAPTERS>), grid, block, 0, st, p);
+  return hipGetLastError();
+}
+
+template <int NB>
+hipError_t launch_nb(const GroupGemmParams& p, hipStream_t st) {
+  const int64_t mean = p.M / p.groups;
+  if (p.low) return mean > 64 ? launch_tile<NB, 4, true>(p, st) : launch_tile<NB, 2, true>(p, st);
+  return mean > 64 ? launch_tile<NB, 4, false>(p, st) : launch_tile<NB, 2, false>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_group_gemm(const GroupGemmParams& p, hipStream_t stream) {
+  switch (p.nbits) {
+    case 2: return launch_nb<2>(p, stream);
+    case 3: return launch_nb<3>(p, stream);
+    case 4: return launch_nb<4>(p, stream);
+    case 8: return launch_nb<8>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace hqq

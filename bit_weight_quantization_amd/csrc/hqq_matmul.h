@@ -23,6 +23,12 @@ struct MatmulParams {
   const int32_t* offsets = nullptr;  // first row of every expert, experts + 1 values
   const int32_t* order = nullptr;    // null: X holds the sorted rows; else row i is X[order[i] / topk]
   int experts = 0, topk = 1;
+  // adapters added by the per-row kernel (LOW): part[split][m][r] sums to A x of row m
+  const float* low = nullptr;        // splits x M x rank, or null
+  int low_splits = 0, rank = 0, adapters = 0;
+  const uint16_t* factor = nullptr;  // adapters x N x rank binary16
+  const int32_t* ids = nullptr;
+  const float* scales = nullptr;
 };
 
 // Rows of X up to which the wavefront-per-row kernel is used (kGemvAlignedMaxRows where
@@ -42,6 +48,17 @@ int64_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits, int g
 
 // `prm.part` must hold matmul_workspace_bytes(...) bytes where that is not 0.
 hipError_t launch_matmul(MatmulParams prm, int cus, hipStream_t stream);
+
+// The product as the base of something added to it, in fp32: either `slabs` partial slabs of
+// `stride` floats in prm.part, to be added in order, or prm.Y (fp32) and slabs = 0.
+struct MatmulBase {
+  int slabs;
+  int64_t stride;
+};
+hipError_t launch_matmul_base(MatmulParams prm, int cus, MatmulBase* base, hipStream_t stream);
+
+// Whether the per-row kernel takes the product and may add adapters itself (prm.low set).
+bool matmul_adds_low(const MatmulParams& prm);
 
 // The products of sorted rows with their experts' weights: prm.offsets set.
 hipError_t launch_matmul_experts(MatmulParams prm, hipStream_t stream);

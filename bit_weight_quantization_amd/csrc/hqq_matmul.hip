@@ -74,7 +74,7 @@ void launch_splitk(MatmulParams P, hipStream_t st) {
   } else {
     launch_splitk_nw<NB, MT, 1>(P, grid, st);
   }
-  if (g.ksplit > 1) {
+  if (g.ksplit > 1 && P.Y) {  // (without Y the slabs are what is wanted)
     int64_t blocks = (P.M * P.N + 4 * kBlock - 1) / (4 * kBlock);
     if (blocks > 4096) blocks = 4096;
     hipLaunchKernelGGL(hqq_splitk_reduce_kernel, dim3((unsigned)blocks), dim3(kBlock), 0, st, P);
@@ -162,6 +162,23 @@ int64_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits, int g
   const SplitGeom g = split_geometry(N, K, nbits);
   if (g.ksplit <= 1) return 0;
   return (int64_t)g.ksplit * ((M * N + 3) & ~(int64_t)3) * (int64_t)sizeof(float);
+}
+
+bool matmul_adds_low(const MatmulParams& prm) {
+  return prm.nbits != 3 && prm.M <= kGemvAlignedMaxRows && prm.K > 0;
+}
+
+hipError_t launch_matmul_base(MatmulParams prm, int cus, MatmulBase* base, hipStream_t stream) {
+  *base = {0, 0};
+  if (prm.nbits != 3 && skinny_aligned(prm) && splitk_shapes(prm.M, prm.K, prm.nbits, prm.group_size)) {
+    const SplitGeom g = split_geometry(prm.N, prm.K, prm.nbits);
+    if (g.ksplit > 1) {
+      *base = {g.ksplit, (prm.M * prm.N + 3) & ~(int64_t)3};
+      prm.Y = nullptr;
+    }
+  }
+  prm.out_f32 = 1;
+  return launch_matmul(prm, cus, stream);
 }
 
 hipError_t launch_matmul(MatmulParams prm, int cus, hipStream_t stream) {

@@ -178,7 +178,10 @@ struct GemvStage {
   uint32_t s[R][kGroups], z[R][kGroups];
 };
 
-template <int NB, int MB, int R, bool G16, bool GROUPED = false>
+//
+// LOW adds an adapter to every row of X: the lanes' sums start with s_a v[r] B_a[n][r], lane r
+// taking every 64th r, and meet in the same butterfly.
+template <int NB, int MB, int R, bool G16, bool GROUPED = false, bool LOW = false>
 __global__ __launch_bounds__(kBlock) void hqq_gemv_packed_kernel(const MatmulParams Pin) {
   const MatmulParams P = group_params<GROUPED>(Pin, 1);
   if (GROUPED && P.M <= 0) return;
@@ -247,6 +250,27 @@ __global__ __launch_bounds__(kBlock) void hqq_gemv_packed_kernel(const MatmulPar
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int m = 0; m < MB; ++m) acc[r][m] = 0.f;
+
+  if constexpr (LOW) {
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const int a = P.ids[m < M ? m : M - 1];
+      if ((uint32_t)a >= (uint32_t)P.adapters) continue;
+      const float s = P.scales[a];
+      const uint16_t* f = P.factor + (int64_t)a * P.N * P.rank;
+      for (int r = lane; r < P.rank; r += kWave) {
+        const float* part = P.low + (int64_t)(m < M ? m : M - 1) * P.rank + r;
+        float v = 0.f;
+        for (int i = 0; i < P.low_splits; ++i) v += part[(int64_t)i * M * P.rank];
+        v *= s;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const int64_t n = n0 + (q < nr ? q : nr - 1);
+          acc[q][m] = __builtin_fmaf(v, h2f(f[n * P.rank + r]), acc[q][m]);
+        }
+      }
+    }
+  }
 
   auto compute = [&](const Stage& cur, bool valid) {
 #pragma unroll
@@ -322,6 +346,11 @@ template <int NB, int R, bool G16>
 void launch_gemv_packed_g(const MatmulParams& P, hipStream_t st) {
   constexpr int kRowsPerBlock = R * (kBlock / kWave);
   const dim3 grid((unsigned)((P.N + kRowsPerBlock - 1) / kRowsPerBlock)), block(kBlock);
+  if (P.low) {
+    if (P.M <= 1) hipLaunchKernelGGL((hqq_gemv_packed_kernel<NB, 1, R, G16, false, true>), grid, block, 0, st, P);
+    else hipLaunchKernelGGL((hqq_gemv_packed_kernel<NB, 2, R, G16, false, true>), grid, block, 0, st, P);
+    return;
+  }
   if (P.M <= 1) hipLaunchKernelGGL((hqq_gemv_packed_kernel<NB, 1, R, G16>), grid, block, 0, st, P);
   else if (P.M <= 2) hipLaunchKernelGGL((hqq_gemv_packed_kernel<NB, 2, R, G16>), grid, block, 0, st, P);
   else if (P.M <= 4) hipLaunchKernelGGL((hqq_gemv_packed_kernel<NB, 4, R, G16>), grid, block, 0, st, P);
@@ -347,13 +376,11 @@ constexpr int kLdsRow = kBK + 8;  // binary16 per LDS row: 144 bytes (16-byte al
 // step's global loads are issued before this step's MFMAs and written to the other buffer
 // after them, with one barrier per step.  Larger TI, TJ read fewer LDS operands per MFMA;
 // a larger WM dequantizes each weight tile for more rows of X.
-template <int NB, int WM, int TI, int TJ, bool GROUPED = false>
+template <int NB, int WM, int TI, int TJ>
 __global__ __launch_bounds__(2 * WM * kWave) __attribute__((amdgpu_waves_per_eu(2)))
-void hqq_gemm_kernel(const MatmulParams Pin) {
+void hqq_gemm_kernel(const MatmulParams P) {
   constexpr int T = 2 * WM * kWave;                 // threads: WM x 2 wavefronts
   constexpr int BM = 32 * TI * WM, BN = 64 * TJ;    // the block's tile
-  const MatmulParams P = group_params<GROUPED>(Pin, BM);
-  if (GROUPED && P.M <= 0) return;
   static_assert(2 * BM == T, "one 32-value item of X per thread and step");
   constexpr int CB = 64 * BN / T;                   // codes per thread and step
   static_assert(CB == 16 || CB == 32, "16 or 32 codes of the weight per thread and step");
@@ -364,7 +391,7 @@ void hqq_gemm_kernel(const MatmulParams Pin) {
   const int tid = threadIdx.x;
   const int wid = tid / kWave, lane = tid & (kWave - 1);
   const int wm = wid >> 1, wn = wid & 1;  // the wavefront's part of the tile
-  const int64_t m0 = GROUPED ? 0 : (int64_t)blockIdx.y * BM, n0 = (int64_t)blockIdx.x * BN;
+  const int64_t m0 = (int64_t)blockIdx.y * BM, n0 = (int64_t)blockIdx.x * BN;
   const int64_t row_bytes = (P.K >> 3) * NB;
   const int64_t gpr = P.K >> P.group_shift;
   const int g2 = P.group_size == 16 ? 1 : 0;
@@ -373,7 +400,7 @@ void hqq_gemm_kernel(const MatmulParams Pin) {
   // outside the matrices become zeros in LDS)
   const int xr = tid >> 1, xh = tid & 1;
   const int br = tid / BP, bp = tid % BP;
-  const uint16_t* xrow = x_row<GROUPED>(P, m0 + xr < P.M ? m0 + xr : P.M - 1);
+  const uint16_t* xrow = P.X + (m0 + xr < P.M ? m0 + xr : P.M - 1) * P.K;
   const int64_t wrow_n = n0 + br < P.N ? n0 + br : P.N - 1;
   const uint8_t* wrow = P.packed + wrow_n * row_bytes;
   const uint16_t* srow = P.scale16 + wrow_n * gpr;
@@ -542,6 +569,11 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void hqq_skinny_general_kerne
 #pragma unroll
     for (int w = 0; w < NW; ++w) acc[t][w] = (float4_t){0.f, 0.f, 0.f, 0.f};
 
+  // the rows of X (looked up once: with an order each is a dependent load and a division)
+  const uint16_t* xrow[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) xrow[t] = x_row<GROUPED>(P, 16 * t + j < P.M ? 16 * t + j : P.M - 1);
+
   // the weight side of block c: per 32-code half h of the lane's slice, the codes and
   // the raw binary16 s, z of both 16-code halves (s = 0 where nothing is loaded)
   struct Wt {
@@ -581,7 +613,7 @@ __global__ __launch_bounds__(kSkinnyWaves * kWave) void hqq_skinny_general_kerne
       for (int t = 0; t < MT; ++t) {
         const int64_t m = 16 * t + j;
         if (kl < P.K && m < P.M) {
-          const uint4* xp = reinterpret_cast<const uint4*>(x_row<GROUPED>(P, m) + kl);
+          const uint4* xp = reinterpret_cast<const uint4*>(xrow[t] + kl);
 #pragma unroll
           for (int i = 0; i < 4; ++i) xr[t][i] = xp[i];
         } else {
@@ -805,13 +837,27 @@ __global__ __launch_bounds__(kSkinnyWaves2 * kWave) void hqq_skinny_kernel(const
   unsigned char* xbuf = lds2 + wid * (2 * MT * 4 * kSlab);
   const int xr = lane >> 4, xg = ((lane & 15) + 4 * xr) & 15;
   lds_u32x4 xs[XS ? MT : 1][8];  // [t][4 half + slab]
+  // GROUPED: the rows' indexes, looked up once
+  int32_t xsi[GROUPED && XS ? MT : 1][4];
+  if constexpr (GROUPED && XS) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int m = 16 * t + 4 * n + xr;
+        const int mm = m < P.M ? m : (int)P.M - 1;
+        xsi[t][n] = P.order ? P.order[mm] / P.topk : mm;
+      }
+  }
   auto load_xs = [&](int64_t c) {
 #pragma unroll
     for (int t = 0; t < (XS ? MT : 0); ++t)
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int64_t m = 16 * t + 4 * n + xr;
-        const uint16_t* g = x_row<GROUPED>(P, m < P.M ? m : P.M - 1) + (c << 8) + 8 * xg;
+        const uint16_t* g;
+        if constexpr (GROUPED) g = P.X + (int64_t)xsi[t][n] * P.K + (c << 8) + 8 * xg;
+        else g = P.X + (m < P.M ? m : P.M - 1) * P.K + (c << 8) + 8 * xg;
         xs[t][n] = *reinterpret_cast<const lds_u32x4*>(g);
         xs[t][4 + n] = *reinterpret_cast<const lds_u32x4*>(g + 128);
       }

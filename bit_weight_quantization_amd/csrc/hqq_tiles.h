@@ -63,6 +63,42 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* offsets, int gro
   return t;
 }
 
+// How many tiles there are in all.  As find_row_tile.
+__device__ __forceinline__ int64_t count_row_tiles(const int32_t* offsets, int groups, int64_t rows,
+                                                   int tile_rows) {
+  const int lane = threadIdx.x & (kWave - 1), last = (int)rows;
+  int64_t total = 0;
+  for (int g0 = 0; g0 <= groups; g0 += kWave) {
+    const int g = g0 + lane;
+    int tiles = 0;
+    if (g <= groups) {
+      const int start = min(max(offsets[g], 0), last);
+      tiles = (max((g < groups ? min(offsets[g + 1], last) : last) - start, 0) + tile_rows - 1) / tile_rows;
+    }
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) tiles += __shfl_xor(tiles, o, kWave);
+    total += tiles;
+  }
+  return total;
+}
+
+// Place of block `id` of a one-dimensional grid among tiles x cols output tiles.  Workgroups go to
+// the 8 XCDs (each with an L2 of its own) in turn, so XCD id % 8 takes one contiguous eighth of an
+// order in which 8 row tiles share a column tile before the next one comes: the blocks that run
+// on one XCD at a time then read few distinct tiles of either operand.
+struct TilePlace {
+  int64_t tile, col;  // tile < 0: no tile for this block
+};
+__device__ __forceinline__ TilePlace place_tile(int64_t id, int64_t tiles, int64_t cols) {
+  constexpr int kXcds = 8, kBand = 8;
+  const int64_t total = tiles * cols, share = (total + kXcds - 1) / kXcds;
+  const int64_t at = id % kXcds * share + id / kXcds;
+  if (id / kXcds >= share || at >= total) return {-1, 0};
+  const int64_t band = at / (kBand * cols), in = at % (kBand * cols);
+  const int64_t left = tiles - band * kBand, high = left < kBand ? left : kBand;
+  return {band * kBand + in % high, in / high};
+}
+
 // The tiles of group `group`: number of its first tile, and how many.  As find_row_tile.
 struct GroupTiles {
   int64_t first;

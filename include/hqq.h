@@ -426,7 +426,7 @@ int64_t hqq_lowrank_workspace_bytes(int64_t rows, int64_t cols, int rank, int ov
  *
  * dY_f16       M x N binary16, row-major, 2-byte aligned.
  * M, N, K      >= 0; K a multiple of group_size and of 32 (else HQQ_ERR_UNSUPPORTED);
- *              M <= 8000000.  M == 0 or K == 0 is a no-op; N == 0 writes zeros.
+ *              M <= 8000000, K <= 2^24.  M == 0 or K == 0 is a no-op; N == 0 writes zeros.
  * packed_codes, scale_f16, zero_f16, nbits, group_size  the N x K weight as for hqq_matmul.
  * dX           M x K row-major: binary16 (out_f32 = 0; 2-byte aligned) or fp32 (out_f32 = 1;
  *              4-byte aligned).
@@ -519,7 +519,8 @@ int hqq_expert_combine_backward(const void* dOut, const void* Ys, int dtype, int
  * X_f16        the rows, K binary16 each, 16-byte aligned: sorted (order_i32 NULL: rows x K), or
  *              the tokens (order_i32 as hqq_expert_sort writes it: row i is X[order[i] / topk];
  *              rows = tokens * topk).
- * rows         0 .. 8000000.  K a multiple of group_size and of 32.  K == 0 writes zeros.
+ * rows         0 .. 8000000.  K a multiple of group_size and of 32, up to 2^24.  K == 0 writes
+ *              zeros.
  * offsets_i32  experts + 1 int32 as hqq_expert_sort writes them.  experts 1 .. 1024.
  * Y            rows x N binary16 or fp32 (out_f32).
  * Other arguments, conventions and errors as for hqq_matmul.
@@ -599,6 +600,41 @@ int hqq_adapters_backward(const void* dY, const void* X, int dtype, int64_t M, i
 
 int64_t hqq_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank,
                                               int adapters);
+
+/*
+ * hqq_matmul_adapters -- hqq_matmul and hqq_adapters in one call, for binary16:
+ *   Y[m] = X[m] Q^-1(W_q)^T + scales[a] * B_a (A_a X[m]),  a = ids[m],
+ * summed in fp32 and rounded once.  One or two rows with 2-, 4- or 8-bit codes add the adapter
+ * inside the per-row product, up to 64 rows after hqq_matmul's product in fp32; more rows are
+ * sorted by adapter, and the matrix-core tiles of the product take the adapters into their
+ * accumulators (A_a X[m] as two binary16 parts, 22 bits of the row's largest value).
+ * workspace    hqq_matmul_adapters_workspace_bytes(...) bytes of device memory, 256-byte aligned.
+ * M <= 4000000, K a multiple of group_size and of 32, up to 2^24.  Other arguments, conventions
+ * and errors as for hqq_matmul (weight) and hqq_adapters (dtype HQQ_DTYPE_F16).
+ */
+int hqq_matmul_adapters(const void* X_f16, int64_t M, int64_t K, const void* packed_codes,
+                        const void* scale_f16, const void* zero_f16, int64_t N, int nbits,
+                        int group_size, const void* A_f16, const void* B_f16, int rank, int adapters,
+                        const void* ids_i32, const void* scales_f32, void* Y, int out_f32,
+                        void* workspace, void* stream);
+
+int64_t hqq_matmul_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits,
+                                            int group_size, int rank, int adapters);
+
+/*
+ * hqq_matmul_adapters_backward -- the gradients of hqq_matmul_adapters for a frozen weight:
+ * hqq_matmul_backward in fp32 as the base of hqq_adapters_backward.
+ * workspace    hqq_matmul_adapters_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+int hqq_matmul_adapters_backward(const void* dY_f16, const void* X_f16, int64_t M, int64_t K,
+                                 const void* packed_codes, const void* scale_f16,
+                                 const void* zero_f16, int64_t N, int nbits, int group_size,
+                                 const void* A_f16, const void* B_f16, int rank, int adapters,
+                                 const void* ids_i32, const void* scales_f32, void* dX, int out_f32,
+                                 void* dA_f32, void* dB_f32, void* workspace, void* stream);
+
+int64_t hqq_matmul_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int nbits,
+                                                     int group_size, int rank, int adapters);
 
 /* Bytes of the packed code stream: rows*cols*nbits/8 (exact for supported
  * shapes).  Returns -1 for invalid arguments or overflow. */

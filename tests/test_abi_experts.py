@@ -42,9 +42,34 @@ CALLS = {
     "hqq_adapters_backward": dict(dY=FAKE, X=FAKE, dtype=0, M=4, K=128, A=FAKE, B=FAKE, N=16, rank=8,
                                   adapters=2, ids_i32=FAKE, scales_f32=FAKE, base=0, base_f32=0,
                                   dX=FAKE, out_f32=0, dA_f32=FAKE, dB_f32=FAKE, workspace=FAKE),
+    "hqq_matmul_adapters": dict(X_f16=FAKE, M=4, K=128, packed_codes=FAKE, scale_f16=FAKE,
+                                zero_f16=FAKE, N=16, nbits=4, group_size=64, A_f16=FAKE, B_f16=FAKE,
+                                rank=8, adapters=2, ids_i32=FAKE, scales_f32=FAKE, Y=FAKE, out_f32=0,
+                                workspace=FAKE),
+    "hqq_matmul_adapters_backward": dict(dY_f16=FAKE, X_f16=FAKE, M=4, K=128, packed_codes=FAKE,
+                                         scale_f16=FAKE, zero_f16=FAKE, N=16, nbits=4, group_size=64,
+                                         A_f16=FAKE, B_f16=FAKE, rank=8, adapters=2, ids_i32=FAKE,
+                                         scales_f32=FAKE, dX=FAKE, out_f32=0, dA_f32=FAKE,
+                                         dB_f32=FAKE, workspace=FAKE),
 }
 
 BAD = {
+    "hqq_matmul_adapters": [
+        (dict(nbits=5), UNS), (dict(group_size=48), UNS), (dict(K=96), INV),
+        (dict(K=48, group_size=16), UNS), (dict(K=1 << 25), INV), (dict(M=-1), INV),
+        (dict(M=4000001), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(rank=12), UNS),
+        (dict(rank=512), UNS), (dict(adapters=0), INV), (dict(adapters=1025), UNS),
+        (dict(X_f16=0), INV), (dict(packed_codes=0), INV), (dict(A_f16=0), INV), (dict(B_f16=0), INV),
+        (dict(ids_i32=0), INV), (dict(scales_f32=0), INV), (dict(Y=0), INV), (dict(workspace=0), INV),
+        (dict(out_f32=2), INV), (dict(X_f16=FAKE + 8), ALN), (dict(packed_codes=FAKE + 8), ALN),
+        (dict(zero_f16=FAKE + 1), ALN), (dict(A_f16=FAKE + 4), ALN), (dict(ids_i32=FAKE + 2), ALN),
+        (dict(Y=FAKE + 2, out_f32=1), ALN), (dict(workspace=FAKE + 64), ALN)],
+    "hqq_matmul_adapters_backward": [
+        (dict(nbits=7), UNS), (dict(K=100), INV), (dict(M=4000001), INV), (dict(rank=4), UNS),
+        (dict(dY_f16=0), INV), (dict(X_f16=0), INV), (dict(scale_f16=0), INV), (dict(dX=0), INV),
+        (dict(dA_f32=0), INV), (dict(dB_f32=0), INV), (dict(workspace=0), INV),
+        (dict(M=0, dA_f32=0), INV), (dict(dY_f16=FAKE + 1), ALN), (dict(dB_f32=FAKE + 8), ALN),
+        (dict(packed_codes=FAKE + 2), ALN), (dict(workspace=FAKE + 4), ALN)],
     "hqq_expert_sort": [
         (dict(tokens=-1), INV), (dict(topk=0), INV), (dict(topk=-3), INV), (dict(experts=0), INV),
         (dict(experts=1025), UNS), (dict(tokens=1 << 31, topk=1), INV),
