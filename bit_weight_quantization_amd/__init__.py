@@ -42,7 +42,7 @@ EXPORTED_SYMBOLS = ("hqq_quantize", "hqq_quantize_ex", "hqq_quantize_batch", "hq
                     "hqq_matmul_backward", "hqq_matmul_backward_workspace_bytes",
                     "hqq_expert_sort", "hqq_expert_sort_workspace_bytes", "hqq_expert_gather",
                     "hqq_expert_combine", "hqq_expert_combine_backward", "hqq_matmul_experts",
-                    "hqq_matmul_experts_backward", "hqq_matmul_experts_backward_workspace_bytes",
+                    "hqq_matmul_experts_workspace_bytes", "hqq_matmul_experts_backward", "hqq_matmul_experts_backward_workspace_bytes",
                     "hqq_adapters", "hqq_adapters_workspace_bytes", "hqq_adapters_backward",
                     "hqq_adapters_backward_workspace_bytes",
                     "hqq_matmul_adapters", "hqq_matmul_adapters_workspace_bytes",
@@ -125,7 +125,7 @@ def load_library(path: str = LIB_PATH):
             ("hqq_expert_gather", [P, I, I64, I, I64, P, P, P]),
             ("hqq_expert_combine", [P, I, I64, I, I64, P, P, P, P]),
             ("hqq_expert_combine_backward", [P, P, I, I64, I, I64, P, P, P, P, P]),
-            ("hqq_matmul_experts", [P, I64, I64, P, I, P, I, P, P, P, I64, I, I, P, I, P]),
+            ("hqq_matmul_experts", [P, I64, I64, P, I, P, I, P, P, P, I64, I, I, P, I, P, P]),
             ("hqq_matmul_experts_backward", [P, I64, I64, P, I, P, P, P, I64, I, I, P, I, P, P]),
             ("hqq_adapters", [P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P]),
             ("hqq_adapters_backward", [P, P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P, P,
@@ -138,6 +138,7 @@ def load_library(path: str = LIB_PATH):
     for name, args in (
             ("hqq_matmul_backward_workspace_bytes", [I64, I64, I64]),
             ("hqq_expert_sort_workspace_bytes", [I64, I, I]),
+            ("hqq_matmul_experts_workspace_bytes", [I64, I64, I64, I]),
             ("hqq_matmul_experts_backward_workspace_bytes", [I64, I64, I64, I]),
             ("hqq_adapters_workspace_bytes", [I64, I64, I64, I, I]),
             ("hqq_adapters_backward_workspace_bytes", [I64, I64, I64, I, I]),
@@ -333,10 +334,15 @@ def hqq_expert_combine_backward(dOut: int, Ys: int, dtype: int, tokens: int, top
 
 def hqq_matmul_experts(X_f16: int, rows: int, K: int, order_i32: int, topk: int, offsets_i32: int,
                        experts: int, packed_codes: int, scale_f16: int, zero_f16: int, N: int,
-                       nbits: int, group_size: int, Y: int, out_f32: int, stream: int = 0) -> int:
+                       nbits: int, group_size: int, Y: int, out_f32: int, workspace: int = 0,
+                       stream: int = 0) -> int:
     return load_library().hqq_matmul_experts(X_f16, rows, K, order_i32, topk, offsets_i32, experts,
                                              packed_codes, scale_f16, zero_f16, N, nbits,
-                                             group_size, Y, out_f32, stream)
+                                             group_size, Y, out_f32, workspace, stream)
+
+
+def hqq_matmul_experts_workspace_bytes(rows: int, N: int, K: int, experts: int) -> int:
+    return load_library().hqq_matmul_experts_workspace_bytes(rows, N, K, experts)
 
 
 def hqq_matmul_experts_backward(dY_f16: int, rows: int, N: int, offsets_i32: int, experts: int,
@@ -1027,7 +1033,7 @@ def _expert_rows(q: "QuantizedWeight", route: ExpertOrder) -> int:
 
 
 def matmul_experts(X, q: "QuantizedWeight", route: ExpertOrder, sorted_rows: bool = False,
-                   out_f32: bool = False, out=None, stream=None):
+                   out_f32: bool = False, out=None, workspace=None, stream=None):
     """The products of the sorted rows with their experts' quantized weights
     (hqq_matmul_experts): rows x N float16 (or float32).  ``q`` holds the experts' N x K weights
     below each other.  ``X`` holds the tokens' rows (float16), or with ``sorted_rows`` the sorted
@@ -1036,13 +1042,17 @@ def matmul_experts(X, q: "QuantizedWeight", route: ExpertOrder, sorted_rows: boo
     dev, K, N = route.order.device, q.cols, _expert_rows(q, route)
     _take(X, "X", torch.float16, (route.rows if sorted_rows else route.tokens, K), dev)
     _weight_on(q, dev)
+    wb = _need(hqq_matmul_experts_workspace_bytes(route.rows, N, K, route.experts),
+               "hqq_matmul_experts")
 
     def call(sh):
         y = _result(out, (route.rows, N), torch.float32 if out_f32 else torch.float16, dev)
+        ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_experts(
             _addr(X), route.rows, K, 0 if sorted_rows else _addr(route.order), route.topk,
             _addr(route.offsets), route.experts, _addr(q.packed), _addr(q.scale), _addr(q.zero), N,
-            q.nbits, q.group_size, _addr(y), int(bool(out_f32)), sh), "hqq_matmul_experts")
+            q.nbits, q.group_size, _addr(y), int(bool(out_f32)), _addr(ws), sh),
+            "hqq_matmul_experts")
         return y
     return _launch(dev, stream, call)
 

@@ -841,7 +841,7 @@ hipError_t launch_adapters_backward(const AdapterParams& p, hipStream_t stream) 
 // product's workspace (few rows), or the base in fp32 and its workspace (backward).
 int64_t matmul_adapters_workspace_bytes(const MatmulParams& q, const AdapterParams& p) {
   const int64_t own = adapters_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters);
-  if (p.M > kFewRows) return own;
+  if (p.M > kFewRows) return own + group_gemm_workspace_bytes(p.M, p.N, p.adapters, true);
   return own + up256(p.M * p.N * (int64_t)sizeof(float)) +
          up256(matmul_workspace_bytes(p.M, p.N, p.K, q.nbits, q.group_size));
 }
@@ -873,7 +873,9 @@ hipError_t launch_matmul_adapters(MatmulParams q, AdapterParams p, int cus, hipS
     g.low = w.v;
     g.factor = p.B;
     g.scales = p.scales;
+    g.ids = p.ids;
     g.rank = p.rank;
+    g.slabs = l.take<float>(0);
     return launch_group_gemm(g, st);
   }
   Layout l{static_cast<char*>(p.workspace)};

@@ -706,7 +706,7 @@ int64_t hqq_matmul_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* order_i32, int topk,
                        const void* offsets_i32, int experts, const void* packed_codes,
                        const void* scale_f16, const void* zero_f16, int64_t N, int nbits,
-                       int group_size, void* Y, int out_f32, void* stream) {
+                       int group_size, void* Y, int out_f32, void* workspace, void* stream) {
   int st = validate_experts(experts);
   if (st != HQQ_OK) return st;
   st = validate_product(rows, N, K, experts, nbits, group_size);
@@ -720,7 +720,12 @@ int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* o
   if (K > 0 && (!aligned(X_f16, 16) || !aligned(packed_codes, 16) || !aligned(scale_f16, 2) ||
                 !aligned(zero_f16, 2)))
     return HQQ_ERR_ALIGNMENT;
+  if (hqq::matmul_experts_workspace_bytes(rows, N, experts) > 0) {
+    if (!workspace) return HQQ_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return HQQ_ERR_ALIGNMENT;
+  }
   hqq::MatmulParams p;
+  p.part = static_cast<float*>(workspace);
   p.X = static_cast<const uint16_t*>(X_f16);
   p.packed = static_cast<const uint8_t*>(packed_codes);
   p.scale16 = static_cast<const uint16_t*>(scale_f16);
@@ -738,6 +743,14 @@ int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* o
   p.experts = experts;
   p.topk = order_i32 ? topk : 1;
   return hqq::launch_matmul_experts(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
+}
+
+int64_t hqq_matmul_experts_workspace_bytes(int64_t rows, int64_t N, int64_t K, int experts) {
+  if (validate_experts(experts) != HQQ_OK || rows > kMaxGroupedRows) return -1;
+  const int64_t n = checked_elems(experts, N);
+  if (n < 0 || checked_elems(rows, K) < 0 || checked_elems(n, K) < 0 || checked_elems(rows, N) < 0)
+    return -1;
+  return rows == 0 || N == 0 ? 0 : hqq::matmul_experts_workspace_bytes(rows, N, experts);
 }
 
 int hqq_matmul_experts_backward(const void* dY_f16, int64_t rows, int64_t N,

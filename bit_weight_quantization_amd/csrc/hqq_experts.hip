@@ -66,6 +66,7 @@ hipError_t launch_tiles(const MatmulParams& P, hipStream_t st) {
   g.order = P.order;
   g.groups = P.experts;
   g.topk = P.topk;
+  g.slabs = P.part;
   return launch_group_gemm(g, st);
 }
 
@@ -82,19 +83,23 @@ hipError_t launch_nb(const MatmulParams& P, hipStream_t st) {
     }
   }
   const int64_t mean = P.M / P.experts;  // rows an expert
+  if (mean > kExpertSkinnyMaxMean) return launch_tiles(P, st);
   if (mean <= 8) launch_skinny<NB, 1>(P, st);
   else if (mean <= 24) launch_skinny<NB, 2>(P, st);
-  else if (mean <= 48) launch_skinny<NB, 4>(P, st);
-  else return launch_tiles(P, st);
+  else launch_skinny<NB, 4>(P, st);
   return hipGetLastError();
 }
 
 }  // namespace
 
+int64_t matmul_experts_workspace_bytes(int64_t M, int64_t N, int64_t experts) {
+  if (M <= kExpertGemvMaxRows || M / experts <= kExpertSkinnyMaxMean) return 0;
+  return group_gemm_workspace_bytes(M, N, experts, false);
+}
+
 hipError_t launch_matmul_experts(MatmulParams prm, hipStream_t stream) {
   prm.ksplit = 1;
   prm.slab = 0;
-  prm.part = nullptr;
   switch (prm.nbits) {
     case 2: return launch_nb<2>(prm, stream);
     case 3: return launch_nb<3>(prm, stream);

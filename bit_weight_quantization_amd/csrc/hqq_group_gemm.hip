@@ -23,6 +23,7 @@ namespace {
 constexpr int kGK = 64;            // k per step
 constexpr int kGRow = kGK + 8;     // halves per LDS row of X (rows 4 banks apart)
 constexpr int kGWaves = 4;
+constexpr int kGUnit = 512;        // unit of splitting k: whole tables of scales for every group size
 constexpr int kGTables = 4;        // ring of the scales' LDS tables, of 4 groups each
 
 constexpr float kSub = 16777216.f;  // 2^24: a binary16 subnormal's unit is 2^-24
@@ -81,24 +82,38 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
   constexpr int XP = BM * kGK / 8 / T;      // 16-byte pieces of X per thread and step
   constexpr int XT = T / (kGK / 8);         // rows of X per round of loads
   constexpr int RC = 64;                    // low-rank values per round (adapters)
-  static_assert(XP >= 1 && 4 * TJ % TI == 0, "a piece per thread at least, decoding in whole pairs");
+  static_assert(XP >= 1 && XP * T * 8 == BM * kGK && 4 * TJ % TI == 0, "a piece per thread at least, decoding in whole pairs");
   constexpr int BN = 32 * TJ * kGWaves;     // weight rows: one per thread
   static_assert(BN == T, "a thread loads the scales of one weight row");
   __shared__ __align__(16) _Float16 As[2][BM][kGRow];
-  __shared__ PairScale Sz[kGTables][4][BN];  // s 2^24 and -s z of the block's rows
+  __shared__ uint32_t Sz[kGTables][4][BN];   // s and z (binary16) of the block's rows
   const int64_t cols = (P.N + BN - 1) / BN;
-  const TilePlace place = place_tile(blockIdx.x, count_row_tiles(P.offsets, P.groups, P.M, BM), cols);
+  const int units = (int)((P.K + kGUnit - 1) / kGUnit);
+  const int64_t tiles = ADAPTERS ? (P.M + BM - 1) / BM : count_row_tiles(P.offsets, P.groups, P.M, BM);
+  const TilePlace place = place_tile(blockIdx.x, tiles, cols, units, P.xcd_slabs);
   if (place.tile < 0) return;
-  const RowTile t = find_row_tile(P.offsets, P.groups, P.M, BM, place.tile);
-  if (t.rows <= 0) return;
+  RowTile t;
+  if constexpr (ADAPTERS) {  // tiles of the sorted rows, across adapters
+    t.group = 0;
+    t.row0 = place.tile * BM;
+    t.rows = (int)(P.M - t.row0 < BM ? P.M - t.row0 : BM);
+  } else {
+    t = find_row_tile(P.offsets, P.groups, P.M, BM, place.tile);
+    if (t.rows <= 0) return;
+  }
   const int tid = threadIdx.x;
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid & (kWave - 1);
   const int i = lane & 31, h = lane >> 5;
   const int64_t n0 = place.col * BN + wid * (32 * TJ);
-  const bool none = t.group == P.groups;
-  const int used = (t.rows + 31) >> 5;  // fragments of 32 rows that hold any
+  // fragments of 32 rows that hold any (none in a wavefront past the last weight row)
+  const int used = n0 < P.N ? (t.rows + 31) >> 5 : 0;
+  const bool none = !ADAPTERS && t.group == P.groups;
   const int64_t w0 = ADAPTERS || none ? 0 : (int64_t)t.group * P.N;
-  const int K = !ADAPTERS && none ? 0 : (int)P.K;  // rows of no expert: zeros
+  const int K = none ? 0 : (int)P.K;  // rows of no expert: zeros
+  // the block's part of the inner size, in whole units
+  const int kfirst = units * place.part / place.parts * kGUnit;
+  const int kend = units * (place.part + 1) / place.parts * kGUnit;
+  const int klast = kend < K ? kend : K;
   const int64_t row_bytes = (P.K >> 3) * NB, gpr = P.K >> P.group_shift;
 
   // rows past the tile read its last row; weight rows past N the last one (results not stored)
@@ -162,8 +177,7 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
     const int table = (k0 >> (P.group_shift + 2)) & (kGTables - 1);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float f = h2f((uint32_t)(s4 >> (16 * c)) & 0xffffu);
-      Sz[table][c][tid] = {f * kSub, -f * h2f((uint32_t)(z4 >> (16 * c)) & 0xffffu)};
+      Sz[table][c][tid] = ((uint32_t)(s4 >> (16 * c)) & 0xffffu) | ((uint32_t)(z4 >> (16 * c)) << 16);
     }
   };
 
@@ -204,10 +218,14 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
   };
   auto read_scales = [&](int k0, Scales& o) {
     const int g = (k0 + 32 * h) >> P.group_shift;
+    auto scales = [&](uint32_t v) -> PairScale {
+      const float f = h2f(v & 0xffffu);
+      return {f * kSub, -f * h2f(v >> 16)};
+    };
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      o.p[j][0] = Sz[(g >> 2) & (kGTables - 1)][g & 3][srow[j]];
-      o.p[j][1] = G16 ? Sz[(g >> 2) & (kGTables - 1)][(g & 3) + 1][srow[j]] : o.p[j][0];
+      o.p[j][0] = scales(Sz[(g >> 2) & (kGTables - 1)][g & 3][srow[j]]);
+      o.p[j][1] = G16 ? scales(Sz[(g >> 2) & (kGTables - 1)][(g & 3) + 1][srow[j]]) : o.p[j][0];
     }
     if (k0 + kGK > K && k0 + 32 * h >= K) {  // the last step's upper half: weights of zero
 #pragma unroll
@@ -221,7 +239,7 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
   // next matrix step's weights (after the last one, of the next step's first); the scheduling
   // barriers keep this order.
   auto step = [&](int buf, int k0, const Codes& cur, Codes& nxt, const Scales& sc, Scales& sn) {
-    const int kn = k0 + kGK < K ? k0 + kGK : 0;  // (past the end: unused)
+    const int kn = k0 + kGK < klast ? k0 + kGK : kfirst;  // (past the end: unused)
     half8_t xf[TI];
     auto read_x = [&](int s, int a) {
       xf[a] = *reinterpret_cast<const half8_t*>(&As[buf][32 * a + i][32 * h + 8 * s]);
@@ -260,59 +278,66 @@ if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
     if (refill) write_scales(k0 + 2 * tk);
     lds_barrier();
   };
-  if (K > 0) {
+  if (kfirst < klast) {
     Codes ca, cb;
     Scales sa, sb;
-    load_x(0);
-    load_codes(0, ca);
-    load_scales(0);
-    write_x(0, 0);
-    write_scales(0);
-    load_scales(tk);
-    write_scales(tk);
+    load_x(kfirst);
+    load_codes(kfirst, ca);
+    load_scales(kfirst);
+    write_x(0, kfirst);
+    write_scales(kfirst);
+    load_scales(kfirst + tk);
+    write_scales(kfirst + tk);
     lds_barrier();
-    read_scales(0, sa);
+    read_scales(kfirst, sa);
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) wf[0][j][e] = decode_pair<NB>(ca.w[j], 0, e, sa.p[j][0]);
-    int k0 = 0;
-    for (; k0 + kGK < K; k0 += 2 * kGK) {
+    int k0 = kfirst;
+    for (; k0 + kGK < klast; k0 += 2 * kGK) {
       step(0, k0, ca, cb, sa, sb);
       step(1, k0 + kGK, cb, ca, sb, sa);
     }
-    if (k0 < K) step(0, k0, ca, cb, sa, sb);
+    if (k0 < klast) step(0, k0, ca, cb, sa, sb);
   }
 
   float back[TI];
 #pragma unroll
   for (int a = 0; a < TI; ++a) back[a] = 1.f;
   if constexpr (ADAPTERS) {
-    // The low-rank product joins the same accumulators: s low[m] enters as two binary16 parts of
+    // The low-rank products join the same accumulators: s low[m] enters as two binary16 parts of
     // the row scaled by a power of two (22 bits below the row's largest value), the accumulators of
-    // the row are scaled alike (exact) and scaled back below.
-    if (!none) {
+    // the row are scaled alike (exact) and scaled back below.  A tile may hold rows of several
+    // adapters: each in turn, with the parts of the other rows left out.
+    const int none_from = P.offsets[P.groups];  // rows of no adapter are behind all others
+    if (place.part == 0 && t.row0 < none_from) {
       __shared__ float scale_up[BM];
+      __shared__ int row_group[BM];
       _Float16* parts = &As[0][0][0];  // [2][BM][RC + 8]: as large as the X buffers
-      const float s = P.scales[t.group];
-      {
-        // 16-byte pieces of row xr + XT p at 4 xp, 4 xp + 32, ..; 8 threads share a row
 #pragma unroll
-        for (int p = 0; p < XP; ++p) {
-          const int m = xr + XT * p;
-          float largest = 0.f;
-          if (m < t.rows)
-            for (int r = xp; r < P.rank; r += 8) {
-              const float v = s * P.low[(t.row0 + m) * P.rank + r];
-              largest = __builtin_isfinite(v) ? __builtin_fmaxf(largest, __builtin_fabsf(v)) : largest;
-            }
+      for (int p = 0; p < XP; ++p) {  // 8 threads share a row
+        const int m = xr + XT * p;
+        int g = -1;
+        if (m < t.rows) {
+          const int32_t o = P.order[t.row0 + m];
+          g = o < 0 ? -1 : P.ids[o];
+        }
+        float largest = 0.f;
+        if (g >= 0)
+          for (int r = xp; r < P.rank; r += 8) {
+            const float v = P.scales[g] * P.low[(t.row0 + m) * P.rank + r];
+            largest = __builtin_isfinite(v) ? __builtin_fmaxf(largest, __builtin_fabsf(v)) : largest;
+          }
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) largest = __builtin_fmaxf(largest, __shfl_xor(largest, o, kWave));
-          // 2^x: the largest comes to [2^13, 2^14); within 2^-40 .. 2^40, so that the accumulators stay
-          // finite (smaller rows then lose what lies below 2^-64)
-          int x = 13 - ((int)((__builtin_bit_cast(uint32_t, largest) >> 23) & 255) - 127);
-          x = x > 40 ? 40 : x < -114 ? -114 : x;
-          if (xp == 0) scale_up[m] = __builtin_bit_cast(float, (uint32_t)(127 + x) << 23);
+        for (int o = 1; o < 8; o <<= 1) largest = __builtin_fmaxf(largest, __shfl_xor(largest, o, kWave));
+        // 2^x: the largest comes to [2^13, 2^14); x within -114 .. 40, so that the accumulators stay
+        // finite (smaller rows then lose what lies below 2^-64)
+        int x = 13 - ((int)((__builtin_bit_cast(uint32_t, largest) >> 23) & 255) - 127);
+        x = x > 40 ? 40 : x < -114 ? -114 : x;
+        if (xp == 0) {
+          scale_up[m] = g >= 0 ? __builtin_bit_cast(float, (uint32_t)(127 + x) << 23) : 1.f;
+          row_group[m] = g;
         }
       }
       __syncthreads();
@@ -325,48 +350,60 @@ if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[a][j][v] *= up;
       }
-      for (int r0 = 0; r0 < P.rank; r0 += RC) {
-        // thread: rows xr + XT p, low-rank values 8 xp .. + 8 of the round
+      for (int m0 = 0; m0 < t.rows;) {  // uniform: the tile's adapters
+        const int g = __builtin_amdgcn_readfirstlane(row_group[m0]);
+        if (g < 0) break;
+        const int64_t gend = P.offsets[g + 1] - t.row0;
+        const int m1 = gend <= m0 ? m0 + 1 : gend < t.rows ? (int)gend : t.rows;  // (past m0 in any case)
+        const float s = P.scales[g];
+        for (int r0 = 0; r0 < P.rank; r0 += RC) {
+          // thread: rows xr + XT p, low-rank values 8 xp .. + 8 of the round
 #pragma unroll
-        for (int p = 0; p < XP; ++p) {
-          const int m = xr + XT * p, r = r0 + 8 * xp;
-          half8_t hi, lo;
-          const float up = s * scale_up[m];
+          for (int p = 0; p < XP; ++p) {
+            const int m = xr + XT * p, r = r0 + 8 * xp;
+            half8_t hi = {}, lo = {};
+            if (m >= m0 && m < m1 && r < P.rank) {
+              const float up = s * scale_up[m];
+              const float* low = P.low + (t.row0 + m) * P.rank + r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = m < t.rows && r < P.rank ? up * P.low[(t.row0 + m) * P.rank + r + e] : 0.f;
-            hi[e] = (_Float16)v;
-            lo[e] = __builtin_isfinite((float)hi[e]) ? (_Float16)(v - (float)hi[e]) : (_Float16)0.f;
+              for (int e = 0; e < 8; ++e) {
+                const float v = up * low[e];
+                hi[e] = (_Float16)v;
+                lo[e] = __builtin_isfinite((float)hi[e]) ? (_Float16)(v - (float)hi[e]) : (_Float16)0.f;
+              }
+            }
+            *reinterpret_cast<half8_t*>(parts + m * kGRow + 8 * xp) = hi;
+            *reinterpret_cast<half8_t*>(parts + (BM + m) * kGRow + 8 * xp) = lo;
           }
-          *reinterpret_cast<half8_t*>(parts + m * kGRow + 8 * xp) = hi;
-          *reinterpret_cast<half8_t*>(parts + (BM + m) * kGRow + 8 * xp) = lo;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int st = 0; st < RC / 16; ++st) {
-          const int r = r0 + 16 * st + 8 * h;
-          if (r0 + 16 * st >= P.rank) break;  // uniform
-          half8_t wf[TJ];
-#pragma unroll
-          for (int j = 0; j < TJ; ++j) {
-            const int64_t n = n0 + 16 * TJ * ((i >> 2) & 1) + 16 * j + 4 * (i >> 3) + (i & 3);
-            wf[j] = (half8_t){};
-            if (n < P.N && r < P.rank)
-              wf[j] = *reinterpret_cast<const half8_t*>(P.factor + ((int64_t)t.group * P.N + n) * P.rank + r);
-          }
-#pragma unroll
-          for (int a = 0; a < TI; ++a) {
-            const _Float16* src = parts + (32 * a + i) * kGRow + 16 * st + 8 * h;
-            const half8_t hi = *reinterpret_cast<const half8_t*>(src);
-            const half8_t lo = *reinterpret_cast<const half8_t*>(src + BM * kGRow);
+          __syncthreads();
+#pragma unroll 1
+          for (int st = 0; st < RC / 16; ++st) {
+            const int r = r0 + 16 * st + 8 * h;
+            if (r0 + 16 * st >= P.rank) break;  // uniform
+            half8_t wl[TJ];
 #pragma unroll
             for (int j = 0; j < TJ; ++j) {
-              acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[j], hi, acc[a][j], 0, 0, 0);
-              acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[j], lo, acc[a][j], 0, 0, 0);
+              const int64_t n = n0 + 16 * TJ * ((i >> 2) & 1) + 16 * j + 4 * (i >> 3) + (i & 3);
+              wl[j] = (half8_t){};
+              if (n < P.N && r < P.rank)
+                wl[j] = *reinterpret_cast<const half8_t*>(P.factor + ((int64_t)g * P.N + n) * P.rank + r);
+            }
+#pragma unroll
+            for (int a = 0; a < TI; ++a) {
+              if (32 * a >= m1 || 32 * a + 32 <= m0) continue;  // uniform: no row of this adapter
+              const _Float16* src = parts + (32 * a + i) * kGRow + 16 * st + 8 * h;
+              const half8_t hi = *reinterpret_cast<const half8_t*>(src);
+              const half8_t lo = *reinterpret_cast<const half8_t*>(src + BM * kGRow);
+#pragma unroll
+              for (int j = 0; j < TJ; ++j) {
+                acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], hi, acc[a][j], 0, 0, 0);
+                acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], lo, acc[a][j], 0, 0, 0);
+              }
             }
           }
+          __syncthreads();
         }
-        __syncthreads();
+        m0 = m1;
       }
     }
   }
@@ -377,6 +414,17 @@ if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
 #pragma unroll
   for (int a = 0; a < TI; ++a) {
     const int m = 32 * a + i;
+    if (place.parts > 1) {  // a part of the sum (rows past the tile too: the slab is the block's own)
+      float* y = P.slabs + ((int64_t)place.slot * BM + m) * BN + wid * (32 * TJ) + 16 * TJ * h;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = back[a] * acc[a][j][e];
+        __builtin_memcpy(y + 16 * j, v, 64);
+      }
+      continue;
+    }
     if (m >= t.rows || n >= P.N) continue;
     int64_t row = t.row0 + m;
     if constexpr (ADAPTERS) {
@@ -415,27 +463,80 @@ if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
   }
 }
 
+// Tiles that were split: the sum of their parts in order.  A block per split tile and 4 rows.
+constexpr int kJoinRows = 4;
+template <int TI, bool ADAPTERS>
+__global__ __launch_bounds__(64 * kGWaves) void hqq_group_gemm_join_kernel(const GroupGemmParams P) {
+  constexpr int BM = 32 * TI, BN = 64 * kGWaves;  // a thread per column
+  const int64_t cols = (P.N + BN - 1) / BN;
+  const int64_t tiles = ADAPTERS ? (P.M + BM - 1) / BM : count_row_tiles(P.offsets, P.groups, P.M, BM);
+  const int xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
+  const TileShare s = tile_share(xcd, tiles * cols, (int)((P.K + kGUnit - 1) / kGUnit));
+  if (rest >= s.rest) return;
+  const TilePlace place = place_at(s.first + s.full + rest, tiles, cols);
+  int64_t row0 = place.tile * BM;
+  int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);
+  if constexpr (!ADAPTERS) {
+    const RowTile t = find_row_tile(P.offsets, P.groups, P.M, BM, place.tile);
+    row0 = t.row0;
+    rows = t.rows;
+  }
+  const int64_t n = place.col * BN + threadIdx.x;
+  if (n >= P.N) return;
+  const float* slab = P.slabs + (int64_t)(xcd * P.xcd_slabs + rest * s.parts) * BM * BN + threadIdx.x;
+  for (int m = blockIdx.y * kJoinRows; m < (int)(blockIdx.y + 1) * kJoinRows && m < rows; ++m) {
+    float part[kMaxParts];
+#pragma unroll
+    for (int p = 0; p < kMaxParts; ++p) part[p] = p < s.parts ? slab[((int64_t)p * BM + m) * BN] : 0.f;
+    float y = part[0];
+#pragma unroll
+    for (int p = 1; p < kMaxParts; ++p) y += part[p];
+    int64_t row = row0 + m;
+    if constexpr (ADAPTERS) {
+      const int32_t o = P.order[row];
+      row = o < 0 ? ~o : o;
+    }
+    if (P.out_f32) static_cast<float*>(P.Y)[row * P.N + n] = y;
+    else static_cast<_Float16*>(P.Y)[row * P.N + n] = (_Float16)y;
+  }
+}
+
+// 128 rows a tile where the groups' mean reaches beyond 64, else 64.
+bool tall_tiles(int64_t M, int64_t groups) { return M / groups > 64; }
+int64_t most_tiles(int64_t M, int64_t N, int64_t groups, bool adapters, int64_t bm) {
+  return (N + 64 * kGWaves - 1) / (64 * kGWaves) * (adapters ? (M + bm - 1) / bm : max_row_tiles(M, groups, bm));
+}
+
 template <int NB, int TI, bool ADAPTERS>
-hipError_t launch_tile(const GroupGemmParams& p, hipStream_t st) {
-  constexpr int kCols = kGWaves * 64;
-  const int64_t blocks = (p.N + kCols - 1) / kCols * max_row_tiles(p.M, p.groups, 32 * TI);
-  const dim3 grid((unsigned)((blocks + 7) & ~(int64_t)7));  // (every XCD its share)
-  const dim3 block(kGWaves * kWave);
+hipError_t launch_tile(GroupGemmParams p, hipStream_t st) {
+  const int64_t most = most_tiles(p.M, p.N, p.groups, ADAPTERS, 32 * TI), blocks = place_blocks(most);
+  p.xcd_slabs = place_slabs(most);
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(kGWaves * kWave);
   if (p.group_shift == 4) hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, true, ADAPTERS>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, false, ADAPTERS>), grid, block, 0, st, p);
+  if (p.K > kGUnit) {  // (one unit of k is never split; fewer than half of an XCD's slots can be split tiles)
+    const dim3 join(kXcds * kXcdSlots / 2, 32 * TI / kJoinRows);
+    hipLaunchKernelGGL((hqq_group_gemm_join_kernel<TI, ADAPTERS>), join, dim3(64 * kGWaves), 0, st, p);
+  }
   return hipGetLastError();
 }
 
 template <int NB>
 hipError_t launch_nb(const GroupGemmParams& p, hipStream_t st) {
-  const int64_t mean = p.M / p.groups;
-  if (p.low) return mean > 64 ? launch_tile<NB, 4, true>(p, st) : launch_tile<NB, 2, true>(p, st);
-  return mean > 64 ? launch_tile<NB, 4, false>(p, st) : launch_tile<NB, 2, false>(p, st);
+  if (p.low) return launch_tile<NB, 4, true>(p, st);
+  return tall_tiles(p.M, p.groups) ? launch_tile<NB, 4, false>(p, st) : launch_tile<NB, 2, false>(p, st);
 }
 
 }  // namespace
 
-hipError_t launch_group_gemm(const GroupGemmParams& p, hipStream_t stream) {
+int64_t group_gemm_workspace_bytes(int64_t M, int64_t N, int64_t groups, bool adapters) {
+  const int64_t bm = adapters || tall_tiles(M, groups) ? 128 : 64;
+  return (int64_t)kXcds * place_slabs(most_tiles(M, N, groups, adapters, bm)) * bm * 64 * kGWaves *
+         (int64_t)sizeof(float);
+}
+
+hipError_t launch_group_gemm(GroupGemmParams p, hipStream_t stream) {
   switch (p.nbits) {
     case 2: return launch_nb<2>(p, stream);
     case 3: return launch_nb<3>(p, stream);

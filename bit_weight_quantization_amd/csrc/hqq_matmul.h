@@ -41,6 +41,8 @@ constexpr int kSkinnyMaxRows = 64;
 constexpr int kSplitMinRows = 16;  // above this (and up to kSkinnyMaxRows) K is split
 // Sorted rows of many experts up to which every row is a product of its own.
 constexpr int kExpertGemvMaxRows = 8;
+// Mean rows of an expert up to which blocks split K over their wavefronts (above: tiles).
+constexpr int kExpertSkinnyMaxMean = 48;
 
 // Bytes of workspace the product needs for these shapes (the split-K partial slabs of
 // the skinny path; 0 when the path writes Y directly).  Depends on the shapes only.
@@ -61,6 +63,8 @@ hipError_t launch_matmul_base(MatmulParams prm, int cus, MatmulBase* base, hipSt
 bool matmul_adds_low(const MatmulParams& prm);
 
 // The products of sorted rows with their experts' weights: prm.offsets set.
+int64_t matmul_experts_workspace_bytes(int64_t M, int64_t N, int64_t experts);
+// `prm.part` must hold matmul_experts_workspace_bytes(...) bytes where that is not 0.
 hipError_t launch_matmul_experts(MatmulParams prm, hipStream_t stream);
 
 }  // namespace hqq

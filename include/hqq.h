@@ -523,12 +523,16 @@ int hqq_expert_combine_backward(const void* dOut, const void* Ys, int dtype, int
  *              zeros.
  * offsets_i32  experts + 1 int32 as hqq_expert_sort writes them.  experts 1 .. 1024.
  * Y            rows x N binary16 or fp32 (out_f32).
+ * workspace    hqq_matmul_experts_workspace_bytes(rows, N, K, experts) bytes of device memory,
+ *              16-byte aligned, or NULL where that is 0 (as for hqq_matmul).
  * Other arguments, conventions and errors as for hqq_matmul.
  */
 int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* order_i32, int topk,
                        const void* offsets_i32, int experts, const void* packed_codes,
                        const void* scale_f16, const void* zero_f16, int64_t N, int nbits,
-                       int group_size, void* Y, int out_f32, void* stream);
+                       int group_size, void* Y, int out_f32, void* workspace, void* stream);
+
+int64_t hqq_matmul_experts_workspace_bytes(int64_t rows, int64_t N, int64_t K, int experts);
 
 /*
  * hqq_matmul_experts_backward -- the gradient of hqq_matmul_experts' sorted rows: dX[i] =

@@ -29,7 +29,7 @@ CALLS = {
                                         dweights_f32=FAKE),
     "hqq_matmul_experts": dict(X_f16=FAKE, rows=8, K=128, order_i32=FAKE, topk=2, offsets_i32=FAKE,
                                experts=4, packed_codes=FAKE, scale_f16=FAKE, zero_f16=FAKE, N=16,
-                               nbits=4, group_size=64, Y=FAKE, out_f32=0),
+                               nbits=4, group_size=64, Y=FAKE, out_f32=0, workspace=0),
     "hqq_matmul_experts_backward": dict(dY_f16=FAKE, rows=8, N=16, offsets_i32=FAKE, experts=4,
                                         packed_codes=FAKE, scale_f16=FAKE, zero_f16=FAKE, K=128,
                                         nbits=4, group_size=64, dX=FAKE, out_f32=0, workspace=FAKE),
@@ -98,7 +98,8 @@ BAD = {
         (dict(scale_f16=0), INV), (dict(zero_f16=0), INV), (dict(Y=0), INV),
         (dict(offsets_i32=0), INV), (dict(X_f16=FAKE + 8), ALN), (dict(packed_codes=FAKE + 4), ALN),
         (dict(scale_f16=FAKE + 1), ALN), (dict(offsets_i32=FAKE + 2), ALN),
-        (dict(order_i32=FAKE + 2), ALN), (dict(Y=FAKE + 2, out_f32=1), ALN)],
+        (dict(order_i32=FAKE + 2), ALN), (dict(Y=FAKE + 2, out_f32=1), ALN),
+        (dict(rows=400), INV), (dict(rows=400, workspace=FAKE + 8), ALN)],
     "hqq_matmul_experts_backward": [
         (dict(nbits=1), UNS), (dict(group_size=256), UNS), (dict(K=96), INV), (dict(experts=-1), INV),
         (dict(experts=1025), UNS), (dict(rows=8000001), INV), (dict(out_f32=-1), INV),
