@@ -7,7 +7,7 @@
 //   dA_a = s_a sum_m u_m x_m^T,  dB_a = s_a sum_m dy_m v_m^T
 // v and u (rank numbers a row) stay in fp32.  Where they meet 16-bit factors or rows on the
 // matrix cores they enter as a sum of 16-bit parts: two binary16 parts of the value scaled by a
-// power of two (22 bits below the largest value of the row, or of the adapter's rows), or two or
+// power of two (22 bits below the largest value of the row, or of a piece of the adapter's rows), or two or
 // three bfloat16 parts (16 or 24 bits), so the products lose nothing that fp32 sums keep.
 //
 // Bound by HBM: rows of X, dY, base and Y once or twice each, used factors once; 2 rank
@@ -188,7 +188,7 @@ struct ShrinkSide {
   const uint16_t* factor;   // adapters x rank x stride
   int64_t width, stride;
   float* out;               // M x rank
-  uint32_t* largest;        // adapters: bits of the largest finite |out| of an adapter (null: not kept)
+  float* largest;           // the largest finite |out| of every tile of 16 rows (null: not kept)
 };
 struct ShrinkParams {
   ShrinkSide side[2];       // blockIdx.z
@@ -198,18 +198,22 @@ struct ShrinkParams {
   int rank, adapters;
 };
 
-constexpr int kShrinkWaves = 8;
+// Wavefronts of a block: as many as the registers and the LDS of the rank allow (their loads in flight
+// are what hides the latency of the few chunks each has).
+constexpr int shrink_waves(int rt) { return rt <= 4 ? 16 : 8; }
 constexpr int kShrinkRows = 16;
 
-// A block per 16 sorted rows of one adapter; its 8 wavefronts take every eighth chunk of 128 of
-// the width and their tiles are added in LDS in order.  Lane i + 16 q holds 32 consecutive
-// values (32 q ..) of row i of both operands, the four matrix steps of a chunk taking 8 each
-// (the instruction's k order is the same for both, so the sum is the same in another order);
-// a row of a chunk is 256 contiguous bytes.  The factor rows are the A operand, so a lane ends
-// with 4 consecutive r of one row.
+// A block per 16 sorted rows of one adapter; its W wavefronts take every W-th chunk of 128 of
+// the width and their tiles are added in LDS in order.  Lane i + 16 q holds 8 values (8 q ..) of row
+// i of both operands for each of a chunk's four matrix steps, so that one load covers 64 contiguous
+// bytes of 16 rows (with 32 consecutive values per lane each load touched 64 pieces of 64 bytes, and
+// the address unit bound the kernel).  The factor rows are the A operand, so a lane ends with 4
+// consecutive r of one row.
 template <typename D, int RT>
-__global__ __launch_bounds__(kShrinkWaves * kWave) void hqq_adapter_shrink_kernel(const ShrinkParams P) {
+__global__ __launch_bounds__(shrink_waves(RT) * kWave) void hqq_adapter_shrink_kernel(const ShrinkParams P) {
+  constexpr int kShrinkWaves = shrink_waves(RT);
   __shared__ float red[kShrinkWaves][RT * 4][kWave];
+  __shared__ float wave_largest[kShrinkWaves];
   const ShrinkSide S = P.side[blockIdx.z];
   const RowTile t = find_row_tile(P.offsets, P.adapters, P.M, kShrinkRows, blockIdx.x);
   if (t.rows <= 0 || t.group == P.adapters) return;
@@ -226,21 +230,55 @@ __global__ __launch_bounds__(kShrinkWaves * kWave) void hqq_adapter_shrink_kerne
   float4_t acc[RT];
 #pragma unroll
   for (int j = 0; j < RT; ++j) acc[j] = (float4_t){0.f, 0.f, 0.f, 0.f};
+  // The next chunk is in flight during this one's products (up to rank 16 its factors too: two sets
+  // of registers); whole chunks take plain loads, the last one may end anywhere.
   const int64_t chunks = (S.width + 127) >> 7;
-  for (int64_t c = wid; c < chunks; c += kShrinkWaves) {
-    const int64_t k = c * 128 + 32 * q;
-    short8_t xv[4];
+  constexpr int FD = RT <= 1 ? 2 : 1;
+  short8_t xv[2][4], fv[FD][4][RT];
+  auto load_x = [&](int64_t c, short8_t (&o)[4]) {
+    const int64_t k = c * 128 + 8 * q;
+    if ((c + 1) * 128 <= S.width) {  // uniform
 #pragma unroll
-    for (int s = 0; s < 4; ++s) xv[s] = load8(x + k + 8 * s, S.width - k - 8 * s);
+      for (int s = 0; s < 4; ++s) __builtin_memcpy(&o[s], x + k + 32 * s, 16);
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) o[s] = load8(x + k + 32 * s, S.width - k - 32 * s);
+    }
+  };
+  auto load_f = [&](int64_t c, short8_t (&o)[4][RT]) {
+    const int64_t k = c * 128 + 8 * q;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const bool on = k + 8 * s < S.width;  // stride >= width rounded up to 8
+      // past the width (a stride holds it rounded up to 8): any values, X has zeros there; the row's first
+      const int64_t at = k + 32 * s < S.width ? k + 32 * s : 0;
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        short8_t fv = {};
-        if (on) fv = *reinterpret_cast<const short8_t*>(f[j] + k + 8 * s);
-        acc[j] = D::mfma(fv, xv[s], acc[j]);
-      }
+      for (int j = 0; j < RT; ++j) o[s][j] = *reinterpret_cast<const short8_t*>(f[j] + at);
+    }
+  };
+  auto products = [&](const short8_t (&xo)[4], const short8_t (&fo)[4][RT]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[j] = D::mfma(fo[s][j], xo[s], acc[j]);
+  };
+  auto chunk = [&](int64_t c, int cur) {
+    const int64_t cn = c + kShrinkWaves;
+    if (cn < chunks) load_x(cn, xv[cur ^ 1]);
+    if constexpr (FD == 2) {
+      if (cn < chunks) load_f(cn, fv[cur ^ 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      products(xv[cur], fv[cur]);
+    } else {
+      load_f(c, fv[0]);
+      products(xv[cur], fv[0]);
+    }
+  };
+  if (wid < chunks) {
+    load_x(wid, xv[0]);
+    if constexpr (FD == 2) load_f(wid, fv[0]);
+    for (int64_t c = wid; c < chunks; c += 2 * kShrinkWaves) {
+      chunk(c, 0);
+      if (c + kShrinkWaves < chunks) chunk(c + kShrinkWaves, 1);
     }
   }
 #pragma unroll
@@ -265,10 +303,16 @@ __global__ __launch_bounds__(kShrinkWaves * kWave) void hqq_adapter_shrink_kerne
       for (int v = 0; v < 4; ++v) largest = __builtin_fmaxf(largest, finite_abs(sum[v]));
     }
   }
-  if (S.largest && wid < RT) {
+  if (S.largest) {
 #pragma unroll
     for (int o = kWave / 2; o > 0; o >>= 1) largest = __builtin_fmaxf(largest, __shfl_xor(largest, o, kWave));
-    if (lane == 0) atomicMax(S.largest + t.group, __builtin_bit_cast(uint32_t, largest));
+    if (lane == 0) wave_largest[wid] = largest;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int w = 1; w < kShrinkWaves; ++w) largest = __builtin_fmaxf(largest, wave_largest[w]);
+      S.largest[blockIdx.x] = largest;
+    }
   }
 }
 
@@ -428,7 +472,6 @@ struct TransposeParams {
   const uint16_t* B;        // adapters x N x rank -> Bt: adapters x rank x Np, zeros behind N
   uint16_t* Bt;
   const int32_t* offsets;
-  uint32_t* largest;        // 2 x adapters, cleared
   int64_t N, K, Np;
   int rank, adapters;
 };
@@ -438,10 +481,9 @@ constexpr int kTransTile = 64;
 // The used adapters' factors transposed, so that the gradients run the forward kernels with the
 // factors' places swapped: 64 x 64 tiles through LDS; blockIdx.z 0: A, 1: B.
 __global__ __launch_bounds__(kBlock) void hqq_adapter_transpose_kernel(const TransposeParams P) {
-  __shared__ uint16_t tile[kTransTile][kTransTile + 2];
+  __shared__ __align__(16) uint16_t tile[kTransTile][kTransTile + 8];  // [column][row]
   const int a = blockIdx.y;
   const bool of_b = blockIdx.z == 1;
-  if (blockIdx.x == 0 && threadIdx.x == 0) P.largest[(of_b ? P.adapters : 0) + a] = 0u;
   if (P.offsets[a + 1] == P.offsets[a]) return;
   const int64_t rows = of_b ? P.N : P.rank, cols = of_b ? P.rank : P.K;
   const int64_t stride = of_b ? P.Np : P.rank;  // of the output's rows
@@ -450,22 +492,29 @@ __global__ __launch_bounds__(kBlock) void hqq_adapter_transpose_kernel(const Tra
   const int64_t r0 = blockIdx.x / ct * kTransTile, c0 = blockIdx.x % ct * kTransTile;
   const uint16_t* in = (of_b ? P.B : P.A) + (int64_t)a * rows * cols;
   uint16_t* out = (of_b ? P.Bt : P.At) + (int64_t)a * cols * stride;
-  const int x = threadIdx.x % kTransTile, y = threadIdx.x / kTransTile;
-  for (int j = y; j < kTransTile; j += kBlock / kTransTile) {
-    const int64_t r = r0 + j, c = c0 + x;
-    tile[j][x] = r < rows && c < cols ? in[r * cols + c] : (uint16_t)0;
+  // 16-byte pieces both ways (cols and stride are multiples of 8): piece x of row y, then y + 32
+  const int x = threadIdx.x % 8, y = threadIdx.x / 8;
+#pragma unroll
+  for (int j = y; j < kTransTile; j += kBlock / 8) {
+    const int64_t r = r0 + j, c = c0 + 8 * x;
+    short8_t v = {};
+    if (r < rows && c < cols) v = *reinterpret_cast<const short8_t*>(in + r * cols + c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[8 * x + e][j] = (uint16_t)v[e];
   }
   __syncthreads();
-  for (int j = y; j < kTransTile; j += kBlock / kTransTile) {
-    const int64_t c = c0 + j, r = r0 + x;
-    if (c < cols && r < stride) out[c * stride + r] = tile[x][j];
+#pragma unroll
+  for (int j = y; j < kTransTile; j += kBlock / 8) {
+    const int64_t c = c0 + j, r = r0 + 8 * x;
+    if (c < cols && r < stride)
+      *reinterpret_cast<short8_t*>(out + c * stride + r) = *reinterpret_cast<const short8_t*>(&tile[j][8 * x]);
   }
 }
 
 struct OuterSide {
   const uint16_t* rows;     // M x width (X or dY)
   const float* low;         // M x rank, sorted (u or v)
-  const uint32_t* largest;  // adapters
+  const float* largest;     // of every tile of kShrinkRows rows
   float* out;               // dA: adapters x rank x width; dB: adapters x width x rank
   float* slabs;             // pieces x rank x width
   int64_t width;
@@ -505,7 +554,14 @@ __global__ __launch_bounds__(kBlock) void hqq_adapter_outer_kernel(const OuterPa
   const int64_t c0 = ((int64_t)blockIdx.x - (of_b ? P.side[0].blocks : 0)) * kOuterCols;
   float up = 1.f, back = P.scales[t.group];
   if constexpr (D::kScaled) {
-    const int x = scale_exponent(__builtin_bit_cast(float, S.largest[t.group]));
+    // one power of two for the piece: its largest value (every wavefront finds the same)
+    const GroupTiles tiles = find_group_tiles(P.offsets, P.M, kShrinkRows, t.group);
+    const float* of_tile = S.largest + tiles.first + (int64_t)t.index * (P.piece / kShrinkRows);
+    float largest = 0.f;
+    for (int n = lane; n * kShrinkRows < t.rows; n += kWave) largest = __builtin_fmaxf(largest, of_tile[n]);
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) largest = __builtin_fmaxf(largest, __shfl_xor(largest, o, kWave));
+    const int x = scale_exponent(largest);
     up = exp2i(x);
     back *= exp2i(-x);
   }
@@ -520,7 +576,11 @@ __global__ __launch_bounds__(kBlock) void hqq_adapter_outer_kernel(const OuterPa
     for (int j = 0; j < 4; ++j) {
       const int m = m0 + dr + 16 * j;
       dv[j] = (short8_t){};
-      if (m < t.rows && c < S.width) dv[j] = load8(S.rows + P.order[t.row0 + m] * S.width + c, S.width - c);
+      if (m < t.rows) {
+        const uint16_t* row = S.rows + P.order[t.row0 + m] * S.width;
+        if (c0 + kOuterCols <= S.width) __builtin_memcpy(&dv[j], row + c, 16);  // uniform: whole pieces
+        else dv[j] = load8(row + c, S.width - c);
+      }
     }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
@@ -653,7 +713,7 @@ int64_t outer_piece(int64_t M, int64_t N, int64_t K) {
 struct BackwardPlan {
   SortedPlan s;
   float* u;
-  uint32_t* largest;
+  float* largest[2];        // of u and v
   uint16_t* At;
   uint16_t* Bt;
   float* slabs_a;
@@ -664,7 +724,7 @@ struct BackwardPlan {
     piece = outer_piece(M, N, K);
     pieces = max_row_tiles(M, adapters, piece);
     u = l.take<float>(M * rank);
-    largest = l.take<uint32_t>(2 * adapters);
+    for (float*& p : largest) p = l.take<float>(max_row_tiles(M, adapters, kShrinkRows));
     At = l.take<uint16_t>((int64_t)adapters * K * rank);
     Bt = l.take<uint16_t>((int64_t)adapters * Np * rank);
     const int64_t slabs = M > piece ? pieces : 0;  // (else every adapter is one piece)
@@ -675,7 +735,7 @@ struct BackwardPlan {
 
 template <typename D>
 hipError_t launch_shrink(const ShrinkParams& p, int sides, hipStream_t st) {
-  const dim3 grid((unsigned)max_row_tiles(p.M, p.adapters, kShrinkRows), 1, (unsigned)sides), block(kShrinkWaves * kWave);
+  const dim3 grid((unsigned)max_row_tiles(p.M, p.adapters, kShrinkRows), 1, (unsigned)sides), block(shrink_waves(p.rank <= 64 ? 4 : 16) * kWave);
   if (p.rank <= 16) hipLaunchKernelGGL((hqq_adapter_shrink_kernel<D, 1>), grid, block, 0, st, p);
   else if (p.rank <= 32) hipLaunchKernelGGL((hqq_adapter_shrink_kernel<D, 2>), grid, block, 0, st, p);
   else if (p.rank <= 64) hipLaunchKernelGGL((hqq_adapter_shrink_kernel<D, 4>), grid, block, 0, st, p);
@@ -771,13 +831,13 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
   if (p.M > 0) {
     const auto tiles = [](int64_t n) { return (n + kTransTile - 1) / kTransTile; };
     const int64_t of_a = tiles(p.rank) * tiles(p.K), of_b = tiles(w.Np) * tiles(p.rank);
-    TransposeParams t = {p.A, w.At, p.B, w.Bt, w.s.offsets, w.largest, p.N, p.K, w.Np, p.rank, p.adapters};
+    TransposeParams t = {p.A, w.At, p.B, w.Bt, w.s.offsets, p.N, p.K, w.Np, p.rank, p.adapters};
     const int64_t most = of_a > of_b ? of_a : of_b;
     hipLaunchKernelGGL(hqq_adapter_transpose_kernel, dim3((unsigned)(most > 0 ? most : 1), (unsigned)p.adapters, 2),
                        dim3(kBlock), 0, st, t);
     ShrinkParams s = {};
-    s.side[0] = {p.X, p.A, p.K, p.K, w.s.v, w.largest + p.adapters};
-    s.side[1] = {p.dY, w.Bt, p.N, w.Np, w.u, w.largest};
+    s.side[0] = {p.X, p.A, p.K, p.K, w.s.v, D::kScaled ? w.largest[1] : nullptr};
+    s.side[1] = {p.dY, w.Bt, p.N, w.Np, w.u, D::kScaled ? w.largest[0] : nullptr};
     s.order = w.s.order;
     s.offsets = w.s.offsets;
     s.M = p.M;
@@ -793,8 +853,8 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
   }
   OuterParams o = {};
   const auto blocks = [](int64_t n) { return (n + kOuterCols - 1) / kOuterCols; };
-  o.side[0] = {p.X, w.u, w.largest, p.dA, w.slabs_a, p.K, blocks(p.K)};
-  o.side[1] = {p.dY, w.s.v, w.largest + p.adapters, p.dB, w.slabs_b, p.N, blocks(p.N)};
+  o.side[0] = {p.X, w.u, w.largest[0], p.dA, w.slabs_a, p.K, blocks(p.K)};
+  o.side[1] = {p.dY, w.s.v, w.largest[1], p.dB, w.slabs_b, p.N, blocks(p.N)};
   o.scales = p.scales;
   o.order = w.s.order;
   o.offsets = w.s.offsets;
@@ -841,7 +901,7 @@ hipError_t launch_adapters_backward(const AdapterParams& p, hipStream_t stream) 
 // product's workspace (few rows), or the base in fp32 and its workspace (backward).
 int64_t matmul_adapters_workspace_bytes(const MatmulParams& q, const AdapterParams& p) {
   const int64_t own = adapters_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters);
-  if (p.M > kFewRows) return own + group_gemm_workspace_bytes(p.M, p.N, p.adapters, true);
+  if (p.M > kFewRows) return own + group_gemm_workspace_bytes(p.M, p.N, p.K, p.adapters, true);
   return own + up256(p.M * p.N * (int64_t)sizeof(float)) +
          up256(matmul_workspace_bytes(p.M, p.N, p.K, q.nbits, q.group_size));
 }
@@ -929,8 +989,7 @@ hipError_t launch_matmul_adapters_backward(const MatmulParams& q, AdapterParams 
     t.group_size = q.group_size;
     t.group_shift = q.group_shift;
     t.out_f32 = 1;
-    t.part = l.take<float>(0);
-    t.nsplit = 1;
+    t.slabs = l.take<float>(0);
     const hipError_t e = launch_matmul_t(t, st);
     if (e != hipSuccess) return e;
     p.base = base;

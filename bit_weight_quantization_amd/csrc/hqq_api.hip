@@ -653,8 +653,8 @@ int matmul_backward(const void* dY, int64_t M, int64_t N, const void* offsets, i
   p.out_f32 = out_f32;
   p.offsets = static_cast<const int32_t*>(offsets);
   p.experts = experts;
-  p.part = static_cast<float*>(workspace);
-  p.nsplit = 1;
+  p.slabs = static_cast<float*>(workspace);
+  p.xcd_slabs = 0;
   return hqq::launch_matmul_t(p, static_cast<hipStream_t>(stream)) == hipSuccess ? HQQ_OK : HQQ_ERR_LAUNCH;
 }
 
@@ -720,7 +720,7 @@ int hqq_matmul_experts(const void* X_f16, int64_t rows, int64_t K, const void* o
   if (K > 0 && (!aligned(X_f16, 16) || !aligned(packed_codes, 16) || !aligned(scale_f16, 2) ||
                 !aligned(zero_f16, 2)))
     return HQQ_ERR_ALIGNMENT;
-  if (hqq::matmul_experts_workspace_bytes(rows, N, experts) > 0) {
+  if (hqq::matmul_experts_workspace_bytes(rows, N, K, experts) > 0) {
     if (!workspace) return HQQ_ERR_INVALID_ARG;
     if (!aligned(workspace, 16)) return HQQ_ERR_ALIGNMENT;
   }
@@ -750,7 +750,7 @@ int64_t hqq_matmul_experts_workspace_bytes(int64_t rows, int64_t N, int64_t K, i
   const int64_t n = checked_elems(experts, N);
   if (n < 0 || checked_elems(rows, K) < 0 || checked_elems(n, K) < 0 || checked_elems(rows, N) < 0)
     return -1;
-  return rows == 0 || N == 0 ? 0 : hqq::matmul_experts_workspace_bytes(rows, N, experts);
+  return rows == 0 || N == 0 ? 0 : hqq::matmul_experts_workspace_bytes(rows, N, K, experts);
 }
 
 int hqq_matmul_experts_backward(const void* dY_f16, int64_t rows, int64_t N,

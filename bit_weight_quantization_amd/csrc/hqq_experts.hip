@@ -92,9 +92,9 @@ hipError_t launch_nb(const MatmulParams& P, hipStream_t st) {
 
 }  // namespace
 
-int64_t matmul_experts_workspace_bytes(int64_t M, int64_t N, int64_t experts) {
+int64_t matmul_experts_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t experts) {
   if (M <= kExpertGemvMaxRows || M / experts <= kExpertSkinnyMaxMean) return 0;
-  return group_gemm_workspace_bytes(M, N, experts, false);
+  return group_gemm_workspace_bytes(M, N, K, experts, false);
 }
 
 hipError_t launch_matmul_experts(MatmulParams prm, hipStream_t stream) {

@@ -29,7 +29,7 @@ struct GroupGemmParams {
   int xcd_slabs;            // slabs of an XCD (set by the launcher)
 };
 
-int64_t group_gemm_workspace_bytes(int64_t M, int64_t N, int64_t groups, bool adapters);
+int64_t group_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, bool adapters);
 
 // experts x N x K weights (p.low null), or one weight and adapters.
 hipError_t launch_group_gemm(GroupGemmParams p, hipStream_t stream);

@@ -23,6 +23,7 @@ namespace {
 constexpr int kGK = 64;            // k per step
 constexpr int kGRow = kGK + 8;     // halves per LDS row of X (rows 4 banks apart)
 constexpr int kGWaves = 4;
+constexpr int kGSlots = 64;        // blocks of an XCD at a time: two per CU
 constexpr int kGUnit = 512;        // unit of splitting k: whole tables of scales for every group size
 constexpr int kGTables = 4;        // ring of the scales' LDS tables, of 4 groups each
 
@@ -90,7 +91,7 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
   const int64_t cols = (P.N + BN - 1) / BN;
   const int units = (int)((P.K + kGUnit - 1) / kGUnit);
   const int64_t tiles = ADAPTERS ? (P.M + BM - 1) / BM : count_row_tiles(P.offsets, P.groups, P.M, BM);
-  const TilePlace place = place_tile(blockIdx.x, tiles, cols, units, P.xcd_slabs);
+  const TilePlace place = place_tile(blockIdx.x, tiles, cols, units, kGSlots, P.xcd_slabs);
   if (place.tile < 0) return;
   RowTile t;
   if constexpr (ADAPTERS) {  // tiles of the sorted rows, across adapters
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(64 * kGWaves) void hqq_group_gemm_join_kernel(const
   const int64_t cols = (P.N + BN - 1) / BN;
   const int64_t tiles = ADAPTERS ? (P.M + BM - 1) / BM : count_row_tiles(P.offsets, P.groups, P.M, BM);
   const int xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
-  const TileShare s = tile_share(xcd, tiles * cols, (int)((P.K + kGUnit - 1) / kGUnit));
+  const TileShare s = tile_share(xcd, tiles * cols, (int)((P.K + kGUnit - 1) / kGUnit), kGSlots);
   if (rest >= s.rest) return;
   const TilePlace place = place_at(s.first + s.full + rest, tiles, cols);
   int64_t row0 = place.tile * BM;
@@ -507,16 +508,24 @@ int64_t most_tiles(int64_t M, int64_t N, int64_t groups, bool adapters, int64_t 
   return (N + 64 * kGWaves - 1) / (64 * kGWaves) * (adapters ? (M + bm - 1) / bm : max_row_tiles(M, groups, bm));
 }
 
+// Whether tiles may be split (adapters: whether any is; experts' tiles are counted on the device; one
+// unit of k is never split).
+bool tiles_split(int64_t M, int64_t N, int64_t K, int64_t groups, bool adapters, int64_t bm) {
+  const int64_t units = (K + kGUnit - 1) / kGUnit;
+  if (units <= 1) return false;
+  return !adapters || place_splits(most_tiles(M, N, groups, true, bm), (int)(units < kMaxParts ? units : kMaxParts), kGSlots);
+}
+
 template <int NB, int TI, bool ADAPTERS>
 hipError_t launch_tile(GroupGemmParams p, hipStream_t st) {
-  const int64_t most = most_tiles(p.M, p.N, p.groups, ADAPTERS, 32 * TI), blocks = place_blocks(most);
-  p.xcd_slabs = place_slabs(most);
+  const int64_t most = most_tiles(p.M, p.N, p.groups, ADAPTERS, 32 * TI), blocks = place_blocks(most, kGSlots);
+  p.xcd_slabs = place_slabs(most, kGSlots);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(kGWaves * kWave);
   if (p.group_shift == 4) hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, true, ADAPTERS>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, false, ADAPTERS>), grid, block, 0, st, p);
-  if (p.K > kGUnit) {  // (one unit of k is never split; fewer than half of an XCD's slots can be split tiles)
-    const dim3 join(kXcds * kXcdSlots / 2, 32 * TI / kJoinRows);
+  if (tiles_split(p.M, p.N, p.K, p.groups, ADAPTERS, 32 * TI)) {  // (split tiles: at most half of an XCD's slots)
+    const dim3 join(kXcds * kGSlots / 2, 32 * TI / kJoinRows);
     hipLaunchKernelGGL((hqq_group_gemm_join_kernel<TI, ADAPTERS>), join, dim3(64 * kGWaves), 0, st, p);
   }
   return hipGetLastError();
@@ -530,9 +539,10 @@ hipError_t launch_nb(const GroupGemmParams& p, hipStream_t st) {
 
 }  // namespace
 
-int64_t group_gemm_workspace_bytes(int64_t M, int64_t N, int64_t groups, bool adapters) {
+int64_t group_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, bool adapters) {
   const int64_t bm = adapters || tall_tiles(M, groups) ? 128 : 64;
-  return (int64_t)kXcds * place_slabs(most_tiles(M, N, groups, adapters, bm)) * bm * 64 * kGWaves *
+  if (!tiles_split(M, N, K, groups, adapters, bm)) return 0;
+  return (int64_t)kXcds * place_slabs(most_tiles(M, N, groups, adapters, bm), kGSlots) * bm * 64 * kGWaves *
          (int64_t)sizeof(float);
 }
 

@@ -63,7 +63,7 @@ hipError_t launch_matmul_base(MatmulParams prm, int cus, MatmulBase* base, hipSt
 bool matmul_adds_low(const MatmulParams& prm);
 
 // The products of sorted rows with their experts' weights: prm.offsets set.
-int64_t matmul_experts_workspace_bytes(int64_t M, int64_t N, int64_t experts);
+int64_t matmul_experts_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t experts);
 // `prm.part` must hold matmul_experts_workspace_bytes(...) bytes where that is not 0.
 hipError_t launch_matmul_experts(MatmulParams prm, hipStream_t stream);
 

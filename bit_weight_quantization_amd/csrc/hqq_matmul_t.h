@@ -17,8 +17,8 @@ struct MatmulTParams {
   int out_f32;
   const int32_t* offsets;   // rows sorted by expert: first row of each; null: one weight
   int experts;
-  float* part;              // nsplit partial slabs of M x K floats (caller's workspace)
-  int nsplit;
+  float* slabs;             // matmul_t_workspace_bytes(...) bytes
+  int xcd_slabs;            // slabs of an XCD (set by the launcher)
 };
 
 int64_t matmul_t_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t experts);

@@ -7,7 +7,7 @@
 // operand, which needs 8 consecutive n of one k in a lane, is read with gfx950's transposing LDS
 // read (ds_read_b64_tr_b16: of each 16 lanes' 4 x 16 block of halves lane i gets column i).
 // Bound by the matrix cores for many rows; for few, by the latency of one block's walk over n,
-// which is then split over blocks and joined in a fixed order.
+// which is then split over blocks and joined in a fixed order (place_tile).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -23,6 +23,8 @@ namespace {
 
 constexpr int kTN = 64;              // n per step
 constexpr int kTK = 128;             // columns (k) of a tile
+constexpr int kTUnit = 8;            // steps in a unit of splitting n
+constexpr int t_slots(int wm) { return wm == 4 ? 32 : 64; }  // blocks of an XCD at a time (LDS: one or two per CU)
 constexpr int kTRowA = kTN + 8;      // halves per LDS row of dY: rows 4 banks apart
 // halves per LDS row of the weight: 320 bytes, so that the four rows of a transposing read
 // start 16 banks apart (of 64) and its 64-byte pieces cover the banks once
@@ -49,9 +51,11 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {  // 2-byte aligned, 
 }
 
 // (64 WM) x 128 output tile per block of 2 WM wavefronts (64 x 64 each: 2 x 2 tiles of
-// v_mfma_f32_32x32x16_f16), n in steps of 64.  Thread t stages row t / 2 of dY (32 values) and
-// CB codes of one weight row per step.  Pipelined as the forward kernel: loads two steps
-// ahead in registers, LDS double-buffered, one LDS-only barrier per step.
+// v_mfma_f32_32x32x16_f16), n in steps of 64.  8 threads stage the 128 bytes of a row of dY, and each
+// thread CB codes of one weight row per step.  Pipelined as the forward kernel: loads two steps
+// ahead in registers, LDS double-buffered, one LDS-only barrier per step.  The weight is the A
+// operand and its row 8 a + 4 h + b stands for column 16 h + 4 a + b of the 32, so that a lane ends
+// with 16 consecutive columns of one row of dX.
 template <int NB, int WM, bool GROUPED>
 __global__ __launch_bounds__(2 * WM * kWave) __attribute__((amdgpu_waves_per_eu(2)))
 void hqq_matmul_t_kernel(const MatmulTParams P) {
@@ -65,24 +69,36 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
   const int tid = threadIdx.x, wid = tid / kWave, lane = tid & (kWave - 1);
   const int wm = wid >> 1, wn = wid & 1;
 
-  int64_t row0 = (int64_t)blockIdx.y * BM;
-  int64_t rows = P.M - row0 < BM ? P.M - row0 : BM;
+  const int64_t cols = (P.K + kTK - 1) / kTK;
+  const int units = (int)((P.N + kTN * kTUnit - 1) / (kTN * kTUnit));
+  const int64_t tiles = GROUPED ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
+  const TilePlace place = place_tile(blockIdx.x, tiles, cols, units, t_slots(WM), P.xcd_slabs);
+  if (place.tile < 0) return;
+  int64_t row0 = place.tile * BM;
+  int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);
   int64_t w0 = 0;                    // first weight row of the expert
   int64_t N = P.N;
   if constexpr (GROUPED) {
-    const RowTile t = find_row_tile(P.offsets, P.experts, P.M, BM, blockIdx.y);
+    const RowTile t = find_row_tile(P.offsets, P.experts, P.M, BM, place.tile);
     if (t.rows <= 0) return;
     row0 = t.row0;
     rows = t.rows;
     w0 = (int64_t)t.group * P.N;
     if (t.group == P.experts) N = 0, w0 = 0;  // rows of no expert: zeros
   }
-  const int64_t k0 = (int64_t)blockIdx.x * kTK;
+  const int64_t k0 = place.col * kTK;
   const int64_t steps = (N + kTN - 1) / kTN;
-  const int64_t st0 = steps * blockIdx.z / P.nsplit, st1 = steps * (blockIdx.z + 1) / P.nsplit;
+  const int64_t st0 = (int64_t)units * place.part / place.parts * kTUnit;
+  const int64_t send = (int64_t)units * (place.part + 1) / place.parts * kTUnit;
+  const int64_t st1 = send < steps ? send : steps;
 
-  const int xr = tid >> 1, xh = tid & 1;
-  const uint16_t* yrow = P.dY + (row0 + (xr < rows ? xr : rows - 1)) * P.N;
+  const int xr = tid >> 3, xp = tid & 7;  // 16-byte piece xp of rows xr + T / 8 i (past the tile: its last row)
+  const uint16_t* yrow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = xr + T / 8 * i;
+    yrow[i] = P.dY + (row0 + (m < rows ? m : rows - 1)) * P.N + 8 * xp;
+  }
   const int br = tid / BP, bp = tid % BP;
   const int64_t kc = k0 + CB * bp < P.K ? k0 + CB * bp : 0;  // (columns past K are not stored)
   const int64_t row_bytes = (P.K >> 3) * NB, gpr = P.K >> P.group_shift;
@@ -94,13 +110,12 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
   auto load_global = [&](auto st_const, int64_t step) {
     constexpr int S = decltype(st_const)::value;
     const int64_t nb = step * kTN;
-    const int64_t ea = nb + 32 * xh;
     if (nb + kTN <= N) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ar[S][i] = load8(yrow + ea + 8 * i);
+      for (int i = 0; i < 4; ++i) ar[S][i] = load8(yrow[i] + nb);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ar[S][i] = load8_part(yrow + ea + 8 * i, N - ea - 8 * i);
+      for (int i = 0; i < 4; ++i) ar[S][i] = load8_part(yrow[i] + nb, N - nb - 8 * xp);
     }
     const int64_t n = nb + br < N ? nb + br : N - 1;
     const uint8_t* cp = P.packed + (w0 + n) * row_bytes;
@@ -129,9 +144,8 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
   };
   auto write_lds = [&](auto st_const, int buf, const uint4 (&bv)[CB / 8]) {
     constexpr int S = decltype(st_const)::value;
-    uint4* ad = reinterpret_cast<uint4*>(&As[buf][xr][32 * xh]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ad[i] = ar[S][i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(&As[buf][xr + T / 8 * i][8 * xp]) = ar[S][i];
     uint4* bd = reinterpret_cast<uint4*>(&Bs[buf][br][CB * bp]);
 #pragma unroll
     for (int i = 0; i < CB / 8; ++i) bd[i] = bv[i];
@@ -145,11 +159,12 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-  // the lane's place in a transposing read: group lane / 16 covers columns 16 (group & 1) .. + 16
-  // of rows 8 (group / 2) .. + 4 (a second read: + 4 .. + 8); lane i of it supplies row i / 4,
-  // columns 4 (i % 4) .. + 4
+  // the lane's place in a transposing read: group lane / 16 = 2 (n half) + (a half), rows n 8 (lane /
+  // 32) .. + 4 (a second read: + 4 .. + 8); lane l of a group supplies row l / 4 and the 4 columns
+  // that lanes 4 (l % 4) .. + 4 of the group take: 16 (l & 1) + 4 (2 (a half) + (l & 3) / 2)
   const int tr_row = 8 * (lane >> 5) + ((lane & 15) >> 2);
-  const int tr_col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const int tr_col = 16 * (lane & 1) + 4 * (2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
+  const bool used0 = wm * 64 < rows;  // wave-uniform
   auto mfma_step = [&](int buf) {
 #pragma unroll
     for (int ks = 0; ks < kTN / 16; ++ks) {
@@ -168,7 +183,7 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[j], af[i], acc[i][j], 0, 0, 0);
     }
   };
   auto step = [&](auto st_const, int64_t c) {
@@ -177,7 +192,7 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
     load_global(st_const, c + 2 < st1 ? c + 2 : st0);
     uint4 bv[CB / 8];
     dequant_b(other, c + 1 < st1 ? c + 1 : st0, bv);
-    mfma_step(S);
+    if (used0) mfma_step(S);  // (a wavefront whose rows are all past the tile only stages)
     write_lds(other, S ^ 1, bv);  // (after the last step: unused)
     lds_barrier();
   };
@@ -198,88 +213,115 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
     }
   }
 
-  float* part = P.nsplit > 1 ? P.part + blockIdx.z * (P.M * P.K) : nullptr;
+  // lane: row lane % 32 of fragment i, columns 32 j + 16 (lane / 32) .. + 16 (K is a multiple of 32)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    const int m = wm * 64 + i * 32 + (lane & 31);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t k = k0 + wn * 64 + j * 32 + (lane & 31);
+      const int c = wn * 64 + j * 32 + 16 * (lane >> 5);
+      float v[16];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t m = wm * 64 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        if (m < rows && k < P.K) {
-          const int64_t at = (row0 + m) * P.K + k;
-          if (part) part[at] = acc[i][j][v];
-          else if (P.out_f32) static_cast<float*>(P.dX)[at] = acc[i][j][v];
-          else static_cast<_Float16*>(P.dX)[at] = (_Float16)acc[i][j][v];
-        }
+      for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
+      if (place.parts > 1) {  // a part of the sum, in the block's own slab
+        __builtin_memcpy(P.slabs + ((int64_t)place.slot * BM + m) * kTK + c, v, 64);
+        continue;
+      }
+      if (m >= rows || k0 + c >= P.K) continue;
+      const int64_t at = (row0 + m) * P.K + k0 + c;
+      if (P.out_f32) {
+        __builtin_memcpy(static_cast<float*>(P.dX) + at, v, 64);
+      } else {
+        _Float16 y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = (_Float16)v[e];
+        __builtin_memcpy(static_cast<_Float16*>(P.dX) + at, y, 32);
       }
     }
   }
 }
 
-// dX = the sum of the nsplit slabs in split order, 4 elements per thread (M K is a multiple of 32).
-__global__ __launch_bounds__(kBlock) void hqq_matmul_t_reduce_kernel(const MatmulTParams P) {
-  typedef float float4_t __attribute__((ext_vector_type(4)));
-  const int64_t mk = P.M * P.K;
-  for (int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 4; i < mk; i += (int64_t)gridDim.x * kBlock * 4) {
-    float4_t y = *reinterpret_cast<const float4_t*>(P.part + i);
-    for (int s = 1; s < P.nsplit; ++s) y += *reinterpret_cast<const float4_t*>(P.part + s * mk + i);
+// Tiles that were split: the sum of their parts in order.  A block per split tile and 8 rows.
+constexpr int kTJoinRows = 8;
+template <int WM, bool GROUPED>
+__global__ __launch_bounds__(kBlock) void hqq_matmul_t_join_kernel(const MatmulTParams P) {
+  constexpr int BM = 64 * WM;
+  const int64_t cols = (P.K + kTK - 1) / kTK;
+  const int64_t tiles = GROUPED ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
+  const int xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
+  const TileShare s = tile_share(xcd, tiles * cols, (int)((P.N + kTN * kTUnit - 1) / (kTN * kTUnit)), t_slots(WM));
+  if (rest >= s.rest) return;
+  const TilePlace place = place_at(s.first + s.full + rest, tiles, cols);
+  int64_t row0 = place.tile * BM;
+  int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);
+  if constexpr (GROUPED) {
+    const RowTile t = find_row_tile(P.offsets, P.experts, P.M, BM, place.tile);
+    row0 = t.row0;
+    rows = t.rows;
+  }
+  const int c = threadIdx.x % kTK;
+  const int64_t k = place.col * kTK + c;
+  if (k >= P.K) return;
+  const float* slab = P.slabs + (int64_t)(xcd * P.xcd_slabs + rest * s.parts) * BM * kTK + c;
+  const int m0 = blockIdx.y * kTJoinRows;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (P.out_f32) static_cast<float*>(P.dX)[i + v] = y[v];
-      else static_cast<_Float16*>(P.dX)[i + v] = (_Float16)y[v];
-    }
+  for (int u = 0; u < kTJoinRows; u += kBlock / kTK) {
+    const int m = m0 + u + threadIdx.x / kTK;
+    if (m >= rows) break;
+    float part[kMaxParts];
+#pragma unroll
+    for (int p = 0; p < kMaxParts; ++p) part[p] = p < s.parts ? slab[((int64_t)p * BM + m) * kTK] : 0.f;
+    float y = part[0];
+#pragma unroll
+    for (int p = 1; p < kMaxParts; ++p) y += part[p];
+    const int64_t at = (row0 + m) * P.K + k;
+    if (P.out_f32) static_cast<float*>(P.dX)[at] = y;
+    else static_cast<_Float16*>(P.dX)[at] = (_Float16)y;
   }
 }
 
-// Tiles of 256 rows from 256 rows an expert on (each weight tile is dequantized once per 256
-// rows), else of 128; the walk over n is split where the tiles alone are fewer than two per CU,
-// into parts of at least 8 steps.  From the shapes alone.
-struct TGeom {
-  int wm, nsplit;
-  int64_t tiles;
-};
-TGeom t_geometry(int64_t M, int64_t N, int64_t K, int64_t experts) {
-  TGeom g;
-  const bool grouped = experts > 0;
-  g.wm = M / (grouped ? experts : 1) >= 256 ? 4 : 2;
-  const int64_t bm = 64 * g.wm;
-  g.tiles = grouped ? max_row_tiles(M, experts, bm) : (M + bm - 1) / bm;
-  const int64_t blocks = g.tiles * ((K + kTK - 1) / kTK);
-  int64_t ns = blocks > 0 ? 512 / blocks : 1;
-  const int64_t most = N / (8 * kTN);
-  if (ns > most) ns = most;
-  g.nsplit = ns < 1 ? 1 : (int)ns;
-  return g;
+// Tiles of 256 rows from a mean of 1024 rows an expert on (each weight tile is dequantized once per 256
+// rows), else of 128 (a group's last tile is half full on average).
+int t_wm(int64_t M, int64_t experts) { return M / (experts > 0 ? experts : 1) >= 1024 ? 4 : 2; }
+int64_t t_most(int64_t M, int64_t K, int64_t experts, int64_t bm) {
+  return (K + kTK - 1) / kTK * (experts > 0 ? max_row_tiles(M, experts, bm) : (M + bm - 1) / bm);
 }
 
-template <int NB, int WM>
-void launch_t(const MatmulTParams& P, int64_t tiles, hipStream_t st) {
-  const dim3 grid((unsigned)((P.K + kTK - 1) / kTK), (unsigned)tiles, (unsigned)P.nsplit), block(2 * WM * kWave);
-  if (P.offsets) hipLaunchKernelGGL((hqq_matmul_t_kernel<NB, WM, true>), grid, block, 0, st, P);
-  else hipLaunchKernelGGL((hqq_matmul_t_kernel<NB, WM, false>), grid, block, 0, st, P);
+// Whether tiles may be split (one weight: whether any is; groups' tiles are counted on the device; one
+// unit of n is never split).
+bool t_splits(int64_t M, int64_t N, int64_t K, int64_t experts, int wm) {
+  const int64_t units = (N + kTN * kTUnit - 1) / (kTN * kTUnit);
+  if (units <= 1) return false;
+  return experts > 0 || place_splits(t_most(M, K, 0, 64 * wm), (int)(units < kMaxParts ? units : kMaxParts), t_slots(wm));
+}
+
+template <int NB, int WM, bool GROUPED>
+hipError_t launch_t(MatmulTParams P, hipStream_t st) {
+  const int64_t most = t_most(P.M, P.K, GROUPED ? P.experts : 0, 64 * WM), blocks = place_blocks(most, t_slots(WM));
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  P.xcd_slabs = place_slabs(most, t_slots(WM));
+  hipLaunchKernelGGL((hqq_matmul_t_kernel<NB, WM, GROUPED>), dim3((unsigned)blocks), dim3(2 * WM * kWave), 0, st, P);
+  if (t_splits(P.M, P.N, P.K, GROUPED ? P.experts : 0, WM)) {  // (split tiles: at most half of an XCD's slots)
+    const dim3 join(kXcds * t_slots(WM) / 2, 64 * WM / kTJoinRows);
+    hipLaunchKernelGGL((hqq_matmul_t_join_kernel<WM, GROUPED>), join, dim3(kBlock), 0, st, P);
+  }
+  return hipGetLastError();
 }
 
 template <int NB>
-hipError_t launch_t_nb(MatmulTParams P, hipStream_t st) {
-  const TGeom g = t_geometry(P.M, P.N, P.K, P.offsets ? P.experts : 0);
-  P.nsplit = g.nsplit;
-  if (g.wm == 4) launch_t<NB, 4>(P, g.tiles, st);
-  else launch_t<NB, 2>(P, g.tiles, st);
-  if (g.nsplit > 1) {
-    int64_t blocks = (P.M * P.K + 4 * kBlock - 1) / (4 * kBlock);
-    if (blocks > 4096) blocks = 4096;
-    hipLaunchKernelGGL(hqq_matmul_t_reduce_kernel, dim3((unsigned)blocks), dim3(kBlock), 0, st, P);
-  }
-  return hipGetLastError();
+hipError_t launch_t_nb(const MatmulTParams& P, hipStream_t st) {
+  if (t_wm(P.M, P.offsets ? P.experts : 0) == 4)
+    return P.offsets ? launch_t<NB, 4, true>(P, st) : launch_t<NB, 4, false>(P, st);
+  return P.offsets ? launch_t<NB, 2, true>(P, st) : launch_t<NB, 2, false>(P, st);
 }
 
 }  // namespace
 
 int64_t matmul_t_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t experts) {
-  const TGeom g = t_geometry(M, N, K, experts);
-  return g.nsplit > 1 ? (int64_t)g.nsplit * M * K * (int64_t)sizeof(float) : 0;
+  const int wm = t_wm(M, experts);
+  if (!t_splits(M, N, K, experts, wm)) return 0;
+  return (int64_t)kXcds * place_slabs(t_most(M, K, experts, 64 * wm), t_slots(wm)) * 64 * wm * kTK *
+         (int64_t)sizeof(float);
 }
 
 hipError_t launch_matmul_t(MatmulTParams prm, hipStream_t stream) {

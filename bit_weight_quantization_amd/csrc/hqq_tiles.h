@@ -83,28 +83,27 @@ __device__ __forceinline__ int64_t count_row_tiles(const int32_t* offsets, int g
 }
 
 // Place of block `id` of a one-dimensional grid among tiles x cols output tiles, for blocks of
-// which a CU holds two.  Workgroups go to the 8 XCDs (each with an L2 of its own) in turn, so XCD
+// which an XCD holds `slots` at a time (its 32 CUs times one or two).  Workgroups go to the 8 XCDs (each with an L2 of its own) in turn, so XCD
 // id % 8 takes one contiguous eighth of an order in which 8 row tiles share a column tile before the
 // next one comes: the blocks that run on one XCD at a time then read few distinct tiles of either
-// operand.  The tiles of an XCD's share that would run alone after its last full round of 64 are
+// operand.  The tiles of an XCD's share that would run alone after its last full round are
 // each split over blocks along the inner size (units of it; at most 8 parts), whose partial sums
 // a second kernel adds in order: a round that is not full costs as much time as a full one.
 constexpr int kXcds = 8, kBand = 8;
-constexpr int kXcdSlots = 64;      // 32 CUs of an XCD, two blocks each
 constexpr int kMaxParts = 8;
 
 struct TileShare {                 // one XCD's part of the order
   int64_t first, full;             // its first place, how many whole tiles
   int rest, parts;                 // tiles behind them, blocks for each
 };
-__device__ __forceinline__ TileShare tile_share(int xcd, int64_t total, int units) {
+__host__ __device__ __forceinline__ TileShare tile_share(int xcd, int64_t total, int units, int slots) {
   TileShare s;
   s.first = total * xcd / kXcds;
   s.full = total * (xcd + 1) / kXcds - s.first;
-  s.rest = (int)(s.full % kXcdSlots);
+  s.rest = (int)(s.full % slots);
   s.parts = 1;
   if (s.rest > 0) {
-    const int most = units < kMaxParts ? units : kMaxParts, fit = kXcdSlots / s.rest;
+    const int most = units < kMaxParts ? units : kMaxParts, fit = slots / s.rest;
     s.parts = fit < most ? fit : most;
   }
   if (s.parts <= 1) s.rest = 0, s.parts = 1;
@@ -122,9 +121,9 @@ __device__ __forceinline__ TilePlace place_at(int64_t at, int64_t tiles, int64_t
   return {band * kBand + in % high, in / high, 0, 1, 0};
 }
 __device__ __forceinline__ TilePlace place_tile(int64_t id, int64_t tiles, int64_t cols, int units,
-                                                int xcd_slabs) {
+                                                int slots, int xcd_slabs) {
   const int xcd = (int)(id % kXcds);
-  const TileShare s = tile_share(xcd, tiles * cols, units);
+  const TileShare s = tile_share(xcd, tiles * cols, units, slots);
   const int64_t at = id / kXcds;
   if (at < s.full) return place_at(s.first + at, tiles, cols);
   const int64_t p = at - s.full;
@@ -135,13 +134,19 @@ __device__ __forceinline__ TilePlace place_tile(int64_t id, int64_t tiles, int64
   t.slot = xcd * xcd_slabs + (int)p;
   return t;
 }
+// Whether any of `total` tiles (the exact number) is split.
+inline bool place_splits(int64_t total, int units, int slots) {
+  for (int x = 0; x < kXcds; ++x)
+    if (tile_share(x, total, units, slots).rest > 0) return true;
+  return false;
+}
 // Blocks that at most `total` tiles need.
-inline int64_t place_blocks(int64_t total) { return ((total + kXcds - 1) / kXcds + kXcdSlots) * kXcds; }
+inline int64_t place_blocks(int64_t total, int slots) { return ((total + kXcds - 1) / kXcds + slots) * kXcds; }
 // Slabs of one XCD's parts where there are at most `total` tiles (its split tiles: at most its share,
 // at most a slot for each part): slab p of XCD x is number x place_slabs(..) + p.
-inline int place_slabs(int64_t total) {
+inline int place_slabs(int64_t total, int slots) {
   const int64_t most = (total + kXcds - 1) / kXcds * kMaxParts;
-  return most < kXcdSlots ? (int)most : kXcdSlots;
+  return most < slots ? (int)most : slots;
 }
 
 // The tiles of group `group`: number of its first tile, and how many.  As find_row_tile.

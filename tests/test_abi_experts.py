@@ -99,7 +99,7 @@ BAD = {
         (dict(offsets_i32=0), INV), (dict(X_f16=FAKE + 8), ALN), (dict(packed_codes=FAKE + 4), ALN),
         (dict(scale_f16=FAKE + 1), ALN), (dict(offsets_i32=FAKE + 2), ALN),
         (dict(order_i32=FAKE + 2), ALN), (dict(Y=FAKE + 2, out_f32=1), ALN),
-        (dict(rows=400), INV), (dict(rows=400, workspace=FAKE + 8), ALN)],
+        (dict(rows=400, K=1024), INV), (dict(rows=400, K=1024, workspace=FAKE + 8), ALN)],
     "hqq_matmul_experts_backward": [
         (dict(nbits=1), UNS), (dict(group_size=256), UNS), (dict(K=96), INV), (dict(experts=-1), INV),
         (dict(experts=1025), UNS), (dict(rows=8000001), INV), (dict(out_f32=-1), INV),
@@ -155,8 +155,8 @@ def test_workspace_sizes():
     for bad in ((-1, 1, 8), (1, 0, 8), (1, 1, 0), (1, 1, 1025), (1 << 31, 1, 8)):
         assert hq.hqq_expert_sort_workspace_bytes(*bad) == -1
     assert hq.hqq_matmul_backward_workspace_bytes(8192, 4096, 4096) == 0   # tiles enough
-    split = hq.hqq_matmul_backward_workspace_bytes(8, 4096, 1024)          # few rows: N is split
-    assert split > 0 and split % (8 * 1024 * 4) == 0
+    assert hq.hqq_matmul_backward_workspace_bytes(8, 4096, 1024) > 0       # few rows: N is split
+    assert hq.hqq_matmul_backward_workspace_bytes(8, 512, 1024) == 0       # too short to split
     assert hq.hqq_matmul_backward_workspace_bytes(-1, 4, 32) == -1
     assert hq.hqq_matmul_experts_backward_workspace_bytes(16, 4096, 1024, 0) == -1
     assert hq.hqq_matmul_experts_backward_workspace_bytes(16, 1 << 60, 1024, 8) == -1
