@@ -294,40 +294,40 @@ def hqq_dequantize(packed_codes: int, scale_f16: int, zero_f16: int, rows: int, 
 def hqq_matmul_backward(dY_f16: int, M: int, N: int, packed_codes: int, scale_f16: int,
                         zero_f16: int, K: int, nbits: int, group_size: int, dX: int, out_f32: int,
                         workspace: int = 0, stream: int = 0) -> int:
-    return load_library().hqq_matmul_backward(dY_f16, M, N, packed_codes, scale_f16, zero_f16, K,
+    return (_lib or load_library()).hqq_matmul_backward(dY_f16, M, N, packed_codes, scale_f16, zero_f16, K,
                                               nbits, group_size, dX, out_f32, workspace, stream)
 
 
 def hqq_matmul_backward_workspace_bytes(M: int, N: int, K: int) -> int:
-    return load_library().hqq_matmul_backward_workspace_bytes(M, N, K)
+    return (_lib or load_library()).hqq_matmul_backward_workspace_bytes(M, N, K)
 
 
 def hqq_expert_sort(ids_i32: int, tokens: int, topk: int, experts: int, order_i32: int,
                     position_i32: int, offsets_i32: int, workspace: int = 0,
                     stream: int = 0) -> int:
-    return load_library().hqq_expert_sort(ids_i32, tokens, topk, experts, order_i32, position_i32,
+    return (_lib or load_library()).hqq_expert_sort(ids_i32, tokens, topk, experts, order_i32, position_i32,
                                           offsets_i32, workspace, stream)
 
 
 def hqq_expert_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
-    return load_library().hqq_expert_sort_workspace_bytes(tokens, topk, experts)
+    return (_lib or load_library()).hqq_expert_sort_workspace_bytes(tokens, topk, experts)
 
 
 def hqq_expert_gather(X: int, dtype: int, tokens: int, topk: int, width: int, position_i32: int,
                       Xs: int, stream: int = 0) -> int:
-    return load_library().hqq_expert_gather(X, dtype, tokens, topk, width, position_i32, Xs, stream)
+    return (_lib or load_library()).hqq_expert_gather(X, dtype, tokens, topk, width, position_i32, Xs, stream)
 
 
 def hqq_expert_combine(Ys: int, dtype: int, tokens: int, topk: int, width: int, position_i32: int,
                        weights_f32: int, out: int, stream: int = 0) -> int:
-    return load_library().hqq_expert_combine(Ys, dtype, tokens, topk, width, position_i32,
+    return (_lib or load_library()).hqq_expert_combine(Ys, dtype, tokens, topk, width, position_i32,
                                              weights_f32, out, stream)
 
 
 def hqq_expert_combine_backward(dOut: int, Ys: int, dtype: int, tokens: int, topk: int, width: int,
                                 position_i32: int, weights_f32: int, dYs: int, dweights_f32: int,
                                 stream: int = 0) -> int:
-    return load_library().hqq_expert_combine_backward(dOut, Ys, dtype, tokens, topk, width,
+    return (_lib or load_library()).hqq_expert_combine_backward(dOut, Ys, dtype, tokens, topk, width,
                                                       position_i32, weights_f32, dYs, dweights_f32,
                                                       stream)
 
@@ -336,64 +336,64 @@ def hqq_matmul_experts(X_f16: int, rows: int, K: int, order_i32: int, topk: int,
                        experts: int, packed_codes: int, scale_f16: int, zero_f16: int, N: int,
                        nbits: int, group_size: int, Y: int, out_f32: int, workspace: int = 0,
                        stream: int = 0) -> int:
-    return load_library().hqq_matmul_experts(X_f16, rows, K, order_i32, topk, offsets_i32, experts,
+    return (_lib or load_library()).hqq_matmul_experts(X_f16, rows, K, order_i32, topk, offsets_i32, experts,
                                              packed_codes, scale_f16, zero_f16, N, nbits,
                                              group_size, Y, out_f32, workspace, stream)
 
 
 def hqq_matmul_experts_workspace_bytes(rows: int, N: int, K: int, experts: int) -> int:
-    return load_library().hqq_matmul_experts_workspace_bytes(rows, N, K, experts)
+    return (_lib or load_library()).hqq_matmul_experts_workspace_bytes(rows, N, K, experts)
 
 
 def hqq_matmul_experts_backward(dY_f16: int, rows: int, N: int, offsets_i32: int, experts: int,
                                 packed_codes: int, scale_f16: int, zero_f16: int, K: int,
                                 nbits: int, group_size: int, dX: int, out_f32: int,
                                 workspace: int = 0, stream: int = 0) -> int:
-    return load_library().hqq_matmul_experts_backward(dY_f16, rows, N, offsets_i32, experts,
+    return (_lib or load_library()).hqq_matmul_experts_backward(dY_f16, rows, N, offsets_i32, experts,
                                                       packed_codes, scale_f16, zero_f16, K, nbits,
                                                       group_size, dX, out_f32, workspace, stream)
 
 
 def hqq_matmul_experts_backward_workspace_bytes(rows: int, N: int, K: int, experts: int) -> int:
-    return load_library().hqq_matmul_experts_backward_workspace_bytes(rows, N, K, experts)
+    return (_lib or load_library()).hqq_matmul_experts_backward_workspace_bytes(rows, N, K, experts)
 
 
 def hqq_adapters(X: int, dtype: int, M: int, K: int, A: int, B: int, N: int, rank: int,
                  adapters: int, ids_i32: int, scales_f32: int, base: int, base_f32: int, Y: int,
                  out_f32: int, workspace: int, stream: int = 0) -> int:
-    return load_library().hqq_adapters(X, dtype, M, K, A, B, N, rank, adapters, ids_i32, scales_f32,
+    return (_lib or load_library()).hqq_adapters(X, dtype, M, K, A, B, N, rank, adapters, ids_i32, scales_f32,
                                        base, base_f32, Y, out_f32, workspace, stream)
 
 
 def hqq_adapters_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
-    return load_library().hqq_adapters_workspace_bytes(M, N, K, rank, adapters)
+    return (_lib or load_library()).hqq_adapters_workspace_bytes(M, N, K, rank, adapters)
 
 
 def hqq_adapters_backward(dY: int, X: int, dtype: int, M: int, K: int, A: int, B: int, N: int,
                           rank: int, adapters: int, ids_i32: int, scales_f32: int, base: int,
                           base_f32: int, dX: int, out_f32: int, dA_f32: int, dB_f32: int,
                           workspace: int, stream: int = 0) -> int:
-    return load_library().hqq_adapters_backward(dY, X, dtype, M, K, A, B, N, rank, adapters, ids_i32,
+    return (_lib or load_library()).hqq_adapters_backward(dY, X, dtype, M, K, A, B, N, rank, adapters, ids_i32,
                                                 scales_f32, base, base_f32, dX, out_f32, dA_f32,
                                                 dB_f32, workspace, stream)
 
 
 def hqq_adapters_backward_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
-    return load_library().hqq_adapters_backward_workspace_bytes(M, N, K, rank, adapters)
+    return (_lib or load_library()).hqq_adapters_backward_workspace_bytes(M, N, K, rank, adapters)
 
 
 def hqq_matmul_adapters(X_f16: int, M: int, K: int, packed_codes: int, scale_f16: int,
                         zero_f16: int, N: int, nbits: int, group_size: int, A_f16: int, B_f16: int,
                         rank: int, adapters: int, ids_i32: int, scales_f32: int, Y: int,
                         out_f32: int, workspace: int, stream: int = 0) -> int:
-    return load_library().hqq_matmul_adapters(X_f16, M, K, packed_codes, scale_f16, zero_f16, N,
+    return (_lib or load_library()).hqq_matmul_adapters(X_f16, M, K, packed_codes, scale_f16, zero_f16, N,
                                               nbits, group_size, A_f16, B_f16, rank, adapters,
                                               ids_i32, scales_f32, Y, out_f32, workspace, stream)
 
 
 def hqq_matmul_adapters_workspace_bytes(M: int, N: int, K: int, nbits: int, group_size: int,
                                         rank: int, adapters: int) -> int:
-    return load_library().hqq_matmul_adapters_workspace_bytes(M, N, K, nbits, group_size, rank,
+    return (_lib or load_library()).hqq_matmul_adapters_workspace_bytes(M, N, K, nbits, group_size, rank,
                                                               adapters)
 
 
@@ -402,14 +402,14 @@ def hqq_matmul_adapters_backward(dY_f16: int, X_f16: int, M: int, K: int, packed
                                  group_size: int, A_f16: int, B_f16: int, rank: int, adapters: int,
                                  ids_i32: int, scales_f32: int, dX: int, out_f32: int, dA_f32: int,
                                  dB_f32: int, workspace: int, stream: int = 0) -> int:
-    return load_library().hqq_matmul_adapters_backward(
+    return (_lib or load_library()).hqq_matmul_adapters_backward(
         dY_f16, X_f16, M, K, packed_codes, scale_f16, zero_f16, N, nbits, group_size, A_f16, B_f16,
         rank, adapters, ids_i32, scales_f32, dX, out_f32, dA_f32, dB_f32, workspace, stream)
 
 
 def hqq_matmul_adapters_backward_workspace_bytes(M: int, N: int, K: int, nbits: int,
                                                  group_size: int, rank: int, adapters: int) -> int:
-    return load_library().hqq_matmul_adapters_backward_workspace_bytes(M, N, K, nbits, group_size,
+    return (_lib or load_library()).hqq_matmul_adapters_backward_workspace_bytes(M, N, K, nbits, group_size,
                                                                        rank, adapters)
 
 
@@ -879,6 +879,9 @@ def _launch(device, stream, call):
 
 def _take(t, name: str, dtype, shape, device):
     """Checks a tensor argument: its type (one, or one of a tuple), shape and device."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.device == device \
+            and (shape is None or t.shape == shape):
+        return t  # (what follows says what is wrong with it)
     if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
@@ -923,11 +926,14 @@ def _result(out, shape, dtype, device):
 
 def _element(t, name: str) -> int:
     import torch
-    code = {torch.float16: HQQ_DTYPE_F16, torch.bfloat16: HQQ_DTYPE_BF16,
-            torch.float32: HQQ_DTYPE_F32}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float16, bfloat16 or float32, not {t.dtype}")
-    return code
+    dt = t.dtype
+    if dt is torch.float16:
+        return HQQ_DTYPE_F16
+    if dt is torch.bfloat16:
+        return HQQ_DTYPE_BF16
+    if dt is torch.float32:
+        return HQQ_DTYPE_F32
+    raise ValueError(f"{name} must be float16, bfloat16 or float32, not {dt}")
 
 
 def _weight_on(q: "QuantizedWeight", device) -> None:
@@ -941,7 +947,7 @@ def expert_sort(ids, experts: int, workspace=None, stream=None) -> ExpertOrder:
     import torch
     if ids.dim() not in (1, 2):
         raise ValueError("ids must be tokens x topk, or flat")
-    dev = _take(ids, "ids", torch.int32, None, None).device
+    dev = _take(ids, "ids", torch.int32, None, ids.device).device
     tokens, topk = ids.shape[0], (ids.shape[1] if ids.dim() == 2 else 1)
     wb = _need(hqq_expert_sort_workspace_bytes(tokens, topk, experts), "hqq_expert_sort")
 
@@ -950,8 +956,8 @@ def expert_sort(ids, experts: int, workspace=None, stream=None) -> ExpertOrder:
         n = tokens * topk
         order, position, offsets = torch.empty(2 * n + experts + 1, dtype=torch.int32,
                                                device=dev).split((n, n, experts + 1))
-        _check_status(hqq_expert_sort(_addr(ids), tokens, topk, experts, _addr(order),
-                                      _addr(position), _addr(offsets), _addr(ws), sh),
+        _check_status(hqq_expert_sort(ids.data_ptr(), tokens, topk, experts, order.data_ptr(),
+                                      position.data_ptr(), offsets.data_ptr(), _addr(ws), sh),
                       "hqq_expert_sort")
         return ExpertOrder(order, position, offsets, tokens, topk, experts)
     return _launch(dev, stream, call)
@@ -968,8 +974,8 @@ def expert_gather(X, route: ExpertOrder, out=None, stream=None):
 
     def call(sh):
         y = _result(out, (route.rows, width), X.dtype, dev)
-        _check_status(hqq_expert_gather(_addr(X), code, route.tokens, route.topk, width,
-                                        _addr(route.position), _addr(y), sh), "hqq_expert_gather")
+        _check_status(hqq_expert_gather(X.data_ptr(), code, route.tokens, route.topk, width,
+                                        route.position.data_ptr(), y.data_ptr(), sh), "hqq_expert_gather")
         return y
     return _launch(dev, stream, call)
 
@@ -995,8 +1001,8 @@ def expert_combine(Ys, route: ExpertOrder, weights=None, out=None, stream=None):
 
     def call(sh):
         y = _result(out, (route.tokens, width), Ys.dtype, dev)
-        _check_status(hqq_expert_combine(_addr(Ys), code, route.tokens, route.topk, width,
-                                         _addr(route.position), _addr(w), _addr(y), sh),
+        _check_status(hqq_expert_combine(Ys.data_ptr(), code, route.tokens, route.topk, width,
+                                         route.position.data_ptr(), _addr(w), y.data_ptr(), sh),
                       "hqq_expert_combine")
         return y
     return _launch(dev, stream, call)
@@ -1020,8 +1026,8 @@ def expert_combine_backward(dOut, Ys, route: ExpertOrder, weights=None, stream=N
         dw = None if w is None else torch.empty((route.tokens, route.topk), dtype=torch.float32,
                                                 device=dev)
         _check_status(hqq_expert_combine_backward(
-            _addr(dOut), _addr(Ys), code, route.tokens, route.topk, width, _addr(route.position),
-            _addr(w), _addr(dYs), _addr(dw), sh), "hqq_expert_combine_backward")
+            dOut.data_ptr(), _addr(Ys), code, route.tokens, route.topk, width, route.position.data_ptr(),
+            _addr(w), dYs.data_ptr(), _addr(dw), sh), "hqq_expert_combine_backward")
         return dYs, dw
     return _launch(dev, stream, call)
 
@@ -1049,9 +1055,9 @@ def matmul_experts(X, q: "QuantizedWeight", route: ExpertOrder, sorted_rows: boo
         y = _result(out, (route.rows, N), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_experts(
-            _addr(X), route.rows, K, 0 if sorted_rows else _addr(route.order), route.topk,
-            _addr(route.offsets), route.experts, _addr(q.packed), _addr(q.scale), _addr(q.zero), N,
-            q.nbits, q.group_size, _addr(y), int(bool(out_f32)), _addr(ws), sh),
+            X.data_ptr(), route.rows, K, 0 if sorted_rows else route.order.data_ptr(), route.topk,
+            route.offsets.data_ptr(), route.experts, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N,
+            q.nbits, q.group_size, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh),
             "hqq_matmul_experts")
         return y
     return _launch(dev, stream, call)
@@ -1072,8 +1078,8 @@ def matmul_experts_backward(dYs, q: "QuantizedWeight", route: ExpertOrder, out_f
         y = _result(out, (route.rows, K), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_experts_backward(
-            _addr(dYs), route.rows, N, _addr(route.offsets), route.experts, _addr(q.packed),
-            _addr(q.scale), _addr(q.zero), K, q.nbits, q.group_size, _addr(y), int(bool(out_f32)),
+            dYs.data_ptr(), route.rows, N, route.offsets.data_ptr(), route.experts, q.packed.data_ptr(),
+            q.scale.data_ptr(), q.zero.data_ptr(), K, q.nbits, q.group_size, y.data_ptr(), int(bool(out_f32)),
             _addr(ws), sh), "hqq_matmul_experts_backward")
         return y
     return _launch(dev, stream, call)
@@ -1095,8 +1101,8 @@ def matmul_backward(dY, q: "QuantizedWeight", out_f32: bool = False, out=None, w
         y = _result(out, (M, q.cols), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_backward(
-            _addr(dY), M, q.rows, _addr(q.packed), _addr(q.scale), _addr(q.zero), q.cols, q.nbits,
-            q.group_size, _addr(y), int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_backward")
+            dY.data_ptr(), M, q.rows, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), q.cols, q.nbits,
+            q.group_size, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_backward")
         return y
     return _launch(dev, stream, call)
 
@@ -1139,8 +1145,8 @@ def adapters(X, A, B, ids, scales, base=None, out_f32: bool = False, out=None, w
         y = _result(out, (M, N), torch.float32 if out_f32 else X.dtype, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_adapters(
-            _addr(X), code, M, K, _addr(A), _addr(B), N, rank, n, _addr(ids), _addr(scales),
-            _addr(base), b32, _addr(y), int(bool(out_f32)), _addr(ws), sh), "hqq_adapters")
+            X.data_ptr(), code, M, K, A.data_ptr(), B.data_ptr(), N, rank, n, ids.data_ptr(), scales.data_ptr(),
+            _addr(base), b32, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh), "hqq_adapters")
         return y
     return _launch(dev, stream, call)
 
@@ -1161,8 +1167,8 @@ def adapters_backward(dY, X, A, B, ids, scales, base=None, out_f32: bool = False
         dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_adapters_backward(
-            _addr(dY), _addr(X), code, M, K, _addr(A), _addr(B), N, rank, n, _addr(ids),
-            _addr(scales), _addr(base), b32, _addr(dX), int(bool(out_f32)), _addr(dA), _addr(dB),
+            dY.data_ptr(), X.data_ptr(), code, M, K, A.data_ptr(), B.data_ptr(), N, rank, n, ids.data_ptr(),
+            scales.data_ptr(), _addr(base), b32, dX.data_ptr(), int(bool(out_f32)), dA.data_ptr(), dB.data_ptr(),
             _addr(ws), sh), "hqq_adapters_backward")
         return dX, dA, dB
     return _launch(dev, stream, call)
@@ -1193,8 +1199,8 @@ def matmul_adapters(X, q: "QuantizedWeight", A, B, ids, scales, out_f32: bool = 
         y = _result(out, (M, N), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_adapters(
-            _addr(X), M, K, _addr(q.packed), _addr(q.scale), _addr(q.zero), N, q.nbits,
-            q.group_size, _addr(A), _addr(B), rank, n, _addr(ids), _addr(scales), _addr(y),
+            X.data_ptr(), M, K, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N, q.nbits,
+            q.group_size, A.data_ptr(), B.data_ptr(), rank, n, ids.data_ptr(), scales.data_ptr(), y.data_ptr(),
             int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_adapters")
         return y
     return _launch(dev, stream, call)
@@ -1217,9 +1223,9 @@ def matmul_adapters_backward(dY, X, q: "QuantizedWeight", A, B, ids, scales, out
         dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_adapters_backward(
-            _addr(dY), _addr(X), M, K, _addr(q.packed), _addr(q.scale), _addr(q.zero), N, q.nbits,
-            q.group_size, _addr(A), _addr(B), rank, n, _addr(ids), _addr(scales), _addr(dX),
-            int(bool(out_f32)), _addr(dA), _addr(dB), _addr(ws), sh),
+            dY.data_ptr(), X.data_ptr(), M, K, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N, q.nbits,
+            q.group_size, A.data_ptr(), B.data_ptr(), rank, n, ids.data_ptr(), scales.data_ptr(), dX.data_ptr(),
+            int(bool(out_f32)), dA.data_ptr(), dB.data_ptr(), _addr(ws), sh),
             "hqq_matmul_adapters_backward")
         return dX, dA, dB
     return _launch(dev, stream, call)

@@ -183,6 +183,48 @@ __device__ __forceinline__ void dequant16(const uint32_t (&w)[Codes16<NB>::kWord
   out[1] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
+constexpr float kSub = 16777216.f;  // 2^24: a binary16 subnormal's unit is 2^-24
+
+// s*q - s*z of two codes as binary16: fma in fp32 (s z exact, one rounding), rounded to binary16.
+// The codes come as the halves of t, each shifted left inside an otherwise empty half: read as
+// binary16 that is a subnormal, q 2^(shift - 24) exactly, and the scales carry the power back.  Two
+// instructions a pair, where conversion in fp32 and a packing conversion take three (and
+// exponents put in front of the codes one more).
+__device__ __forceinline__ uint32_t weight_pair(uint32_t t, float s_lo, float s_hi, float minus_sz) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, %4 op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixhi_f16 %0, %1, %3, %4 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+      : "=&v"(d) : "v"(t), "v"(s_lo), "v"(s_hi), "v"(minus_sz));
+  return d;
+}
+
+// A group's scales as decode_pair takes them: s 2^24 and -s z; the other shifts' powers of s.
+struct PairScale {
+  float a, c;
+};
+
+// Codes 8 step + 2 e and + 1 of a lane's 32 (LSB first in w) as two binary16 weights.
+template <int NB>
+__device__ __forceinline__ uint32_t decode_pair(const uint32_t (&w)[NB], int step, int e, PairScale p) {
+  if constexpr (NB == 3) {         // codes straddle bytes: one by one
+    const float sv = p.a * (1.f / kSub);
+    const float w0 = __builtin_fmaf(sv, (float)code_at<NB>(w, 8 * step + 2 * e), p.c);
+    const float w1 = __builtin_fmaf(sv, (float)code_at<NB>(w, 8 * step + 2 * e + 1), p.c);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t){w0, w1}, half2_t));
+  } else if constexpr (NB == 8) {  // bytes 2 e, 2 e + 1 of two words
+    const uint32_t t = __builtin_amdgcn_perm(0u, w[2 * step + (e >> 1)], (e & 1) ? 0x0C030C02u : 0x0C010C00u);
+    return weight_pair(t, p.a, p.a, p.c);
+  } else if constexpr (NB == 4) {  // byte e of a word, in both halves
+    const uint32_t t = __builtin_amdgcn_perm(0u, w[step], 0x0C000C00u | (uint32_t)e | ((uint32_t)e << 16));
+    return weight_pair(t & 0x00F0000Fu, p.a, p.a * (1.f / 16.f), p.c);
+  } else {                         // byte 2 (step % 2) + e / 2 of a word, two of its four codes
+    const uint32_t at = (uint32_t)(2 * (step & 1) + (e >> 1));
+    const uint32_t t = __builtin_amdgcn_perm(0u, w[step >> 1], 0x0C000C00u | at | (at << 16));
+    return e & 1 ? weight_pair(t & 0x00C00030u, p.a * (1.f / 16.f), p.a * (1.f / 64.f), p.c)
+                 : weight_pair(t & 0x000C0003u, p.a, p.a * (1.f / 4.f), p.c);
+  }
+}
+
 // Block barrier that orders LDS accesses only: __syncthreads() also makes every wavefront
 // wait for its outstanding global loads (vmcnt(0)), which would end each prefetch at
 // the barrier.  The workgroup fences here are restricted to the LDS address space.

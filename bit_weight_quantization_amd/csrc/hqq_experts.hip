@@ -84,7 +84,11 @@ hipError_t launch_nb(const MatmulParams& P, hipStream_t st) {
   }
   const int64_t mean = P.M / P.experts;  // rows an expert
   if (mean > kExpertSkinnyMaxMean) return launch_tiles(P, st);
-  if (mean <= 8) launch_skinny<NB, 1>(P, st);
+  // One 16-row tile a block while a second walk over an expert's codes costs less than the registers
+  // and LDS of two tiles: 8 experts of 4096 x 11008, mean 12 / 16 / 24 rows, one tile against two:
+  // 75 / 97 / 111 and 79 / 80 / 94 us (2 bits), 69 / 89 / 102 and 95 / 100 / 122 us (4 bits).
+  constexpr int64_t kOneTile = NB == 2 ? 12 : NB == 3 ? 8 : 24;
+  if (mean <= kOneTile) launch_skinny<NB, 1>(P, st);
   else if (mean <= 24) launch_skinny<NB, 2>(P, st);
   else launch_skinny<NB, 4>(P, st);
   return hipGetLastError();
