@@ -328,11 +328,11 @@ struct ExpandParams {
   int rank, adapters, base_f32, out_f32;
 };
 
-constexpr int kExpandRows = 64;
+constexpr int kExpandRows = 32;
 constexpr int kExpandCols = 64;  // outputs per wavefront
 constexpr int kExpandWaves = 4;
 
-// out = base + s low factor^T.  A block per 64 sorted rows of one adapter and 256 outputs; a
+// out = base + s low factor^T.  A block per 32 sorted rows of one adapter and 256 outputs; a
 // wavefront keeps its 64 factor rows in registers for the tile's rows.  The factor rows are the
 // A operand, and row 4 q + v of its tile t stands for output 16 q + 4 t + v of the 64, so a lane
 // holds 16 consecutive outputs of one row: base and out move in 16-byte pieces, 64 outputs of a
@@ -346,6 +346,7 @@ __global__ __launch_bounds__(kExpandWaves * kWave) void hqq_adapter_expand_kerne
   const int64_t n0 = ((int64_t)blockIdx.x * kExpandWaves + wid) * kExpandCols;
   if (n0 >= P.width) return;  // wave-uniform; no barrier below
   const bool has = t.group < P.adapters;
+  const bool whole = n0 + kExpandCols <= P.width;
   const float s = has ? P.scales[t.group] : 0.f;
   short8_t f[RS][4];
 #pragma unroll
@@ -362,6 +363,28 @@ __global__ __launch_bounds__(kExpandWaves * kWave) void hqq_adapter_expand_kerne
   for (int m0 = 0; m0 < t.rows; m0 += 16) {
     const int m = m0 + i;
     const bool on = m < t.rows;
+    // the base first: in flight during the products
+    const int32_t o = P.order[t.row0 + (on ? m : 0)];
+    const int64_t at = (int64_t)(o < 0 ? ~o : o) * P.width + n, left = P.width - n;
+    float y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = 0.f;
+    if (P.base && whole) {  // uniform
+      if (P.base_f32) {
+        __builtin_memcpy(y, static_cast<const float*>(P.base) + at, 64);
+      } else {
+        short8_t w[2];
+        __builtin_memcpy(w, static_cast<const uint16_t*>(P.base) + at, 32);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = D::up((uint16_t)w[e >> 3][e & 7]);
+      }
+    } else if (P.base) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (e >= left) continue;
+        y[e] = P.base_f32 ? static_cast<const float*>(P.base)[at + e] : D::up(static_cast<const uint16_t*>(P.base)[at + e]);
+      }
+    }
     float4_t acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = (float4_t){0.f, 0.f, 0.f, 0.f};
@@ -409,32 +432,6 @@ __global__ __launch_bounds__(kExpandWaves * kWave) void hqq_adapter_expand_kerne
       }
     }
     if (!on || n >= P.width) continue;
-    const int32_t o = P.order[t.row0 + m];
-    const int64_t at = (int64_t)(o < 0 ? ~o : o) * P.width + n;
-    float y[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = 0.f;
-    const int64_t left = P.width - n;
-    if (P.base) {
-      if (P.base_f32) {
-        const float* b = static_cast<const float*>(P.base) + at;
-        if (left >= 16) {
-          __builtin_memcpy(y, b, 64);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < left) y[e] = b[e];
-        }
-      } else {
-        const uint16_t* b = static_cast<const uint16_t*>(P.base) + at;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const short8_t w = load8(b + 8 * h, left - 8 * h);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[8 * h + e] = D::up((uint16_t)w[e]);
-        }
-      }
-    }
     if (has) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[e] = __builtin_fmaf(back, acc[e >> 2][e & 3], y[e]);
@@ -845,11 +842,6 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
     s.adapters = p.adapters;
     e = launch_shrink<D>(s, 2, st);
     if (e != hipSuccess) return e;
-    if (p.K > 0) {
-      e = launch_expand<D>({w.u, w.At, p.scales, w.s.order, w.s.offsets, p.base, p.out, p.M, p.K, p.rank,
-                            p.adapters, p.base_f32, p.out_f32}, st);
-      if (e != hipSuccess) return e;
-    }
   }
   OuterParams o = {};
   const auto blocks = [](int64_t n) { return (n + kOuterCols - 1) / kOuterCols; };
@@ -862,9 +854,12 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
   o.rank = p.rank;
   o.adapters = p.adapters;
   o.piece = (int)w.piece;
-  if (o.side[0].blocks + o.side[1].blocks == 0) return hipSuccess;
   if (p.M > 0) {
+    // right behind the first step, while the cache may still hold the rows it read
     e = launch_outer<D>(o, st);
+    if (e != hipSuccess) return e;
+    e = launch_expand<D>({w.u, w.At, p.scales, w.s.order, w.s.offsets, p.base, p.out, p.M, p.K, p.rank,
+                          p.adapters, p.base_f32, p.out_f32}, st);
     if (e != hipSuccess) return e;
   }
   const int64_t most_elems = (p.N > p.K ? p.N : p.K) * p.rank;

@@ -598,7 +598,7 @@ int hqq_meta_dequantize(const void* codes_u8, const void* mscale_f16, const void
 namespace {
 
 constexpr int64_t kMaxGroupedRows = 8000000;  // row tiles of the grid's second dimension
-constexpr int64_t kMaxAdapterRows = 4000000;
+constexpr int64_t kMaxAdapterRows = 2000000;
 constexpr int64_t kMaxInner = 1 << 24;        // K: 64 weight rows stay within 32-bit offsets
 
 int group_shift_of(int group_size) {

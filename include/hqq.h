@@ -559,7 +559,7 @@ int64_t hqq_matmul_experts_backward_workspace_bytes(int64_t rows, int64_t N, int
  * dot products, above on the matrix cores, where A_a X[m] enters as two binary16 parts (22 bits
  * of the row's largest value) or as bfloat16 parts (16 bits, 24 for an fp32 output).
  *
- * X            M x K elements of dtype HQQ_DTYPE_F16 or HQQ_DTYPE_BF16.  0 <= M <= 4000000.
+ * X            M x K elements of dtype HQQ_DTYPE_F16 or HQQ_DTYPE_BF16.  0 <= M <= 2000000.
  * A            adapters x rank x K elements, B: adapters x N x rank elements, of `dtype`.
  * N, K         > 0, K a multiple of 8.  rank a multiple of 8, up to 256 (else
  *              HQQ_ERR_UNSUPPORTED; a smaller rank is padded with zeros).  adapters 1 .. 1024.
@@ -613,7 +613,7 @@ int64_t hqq_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, i
  * sorted by adapter, and the matrix-core tiles of the product take the adapters into their
  * accumulators (A_a X[m] as two binary16 parts, 22 bits of the row's largest value).
  * workspace    hqq_matmul_adapters_workspace_bytes(...) bytes of device memory, 256-byte aligned.
- * M <= 4000000, K a multiple of group_size and of 32, up to 2^24.  Other arguments, conventions
+ * M <= 2000000, K a multiple of group_size and of 32, up to 2^24.  Other arguments, conventions
  * and errors as for hqq_matmul (weight) and hqq_adapters (dtype HQQ_DTYPE_F16).
  */
 int hqq_matmul_adapters(const void* X_f16, int64_t M, int64_t K, const void* packed_codes,

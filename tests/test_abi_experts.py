@@ -57,7 +57,7 @@ BAD = {
     "hqq_matmul_adapters": [
         (dict(nbits=5), UNS), (dict(group_size=48), UNS), (dict(K=96), INV),
         (dict(K=48, group_size=16), UNS), (dict(K=1 << 25), INV), (dict(M=-1), INV),
-        (dict(M=4000001), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(rank=12), UNS),
+        (dict(M=2000001), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(rank=12), UNS),
         (dict(rank=512), UNS), (dict(adapters=0), INV), (dict(adapters=1025), UNS),
         (dict(X_f16=0), INV), (dict(packed_codes=0), INV), (dict(A_f16=0), INV), (dict(B_f16=0), INV),
         (dict(ids_i32=0), INV), (dict(scales_f32=0), INV), (dict(Y=0), INV), (dict(workspace=0), INV),
@@ -65,7 +65,7 @@ BAD = {
         (dict(zero_f16=FAKE + 1), ALN), (dict(A_f16=FAKE + 4), ALN), (dict(ids_i32=FAKE + 2), ALN),
         (dict(Y=FAKE + 2, out_f32=1), ALN), (dict(workspace=FAKE + 64), ALN)],
     "hqq_matmul_adapters_backward": [
-        (dict(nbits=7), UNS), (dict(K=100), INV), (dict(M=4000001), INV), (dict(rank=4), UNS),
+        (dict(nbits=7), UNS), (dict(K=100), INV), (dict(M=2000001), INV), (dict(rank=4), UNS),
         (dict(dY_f16=0), INV), (dict(X_f16=0), INV), (dict(scale_f16=0), INV), (dict(dX=0), INV),
         (dict(dA_f32=0), INV), (dict(dB_f32=0), INV), (dict(workspace=0), INV),
         (dict(M=0, dA_f32=0), INV), (dict(dY_f16=FAKE + 1), ALN), (dict(dB_f32=FAKE + 8), ALN),
@@ -114,7 +114,7 @@ BAD = {
         (dict(scale_f16=0), INV), (dict(dY_f16=FAKE + 1), ALN), (dict(zero_f16=FAKE + 1), ALN),
         (dict(workspace=0), INV), (dict(workspace=FAKE + 4), ALN)],
     "hqq_adapters": [
-        (dict(dtype=2), UNS), (dict(dtype=-1), UNS), (dict(M=-1), INV), (dict(M=4000001), INV),
+        (dict(dtype=2), UNS), (dict(dtype=-1), UNS), (dict(M=-1), INV), (dict(M=2000001), INV),
         (dict(N=0), INV), (dict(K=0), INV), (dict(K=100), UNS), (dict(rank=0), INV),
         (dict(rank=12), UNS), (dict(rank=264), UNS), (dict(adapters=0), INV),
         (dict(adapters=1025), UNS), (dict(N=1 << 58), INV), (dict(X=0), INV), (dict(A=0), INV),
@@ -125,7 +125,7 @@ BAD = {
         (dict(ids_i32=FAKE + 1), ALN), (dict(scales_f32=FAKE + 2), ALN), (dict(base=FAKE + 1), ALN),
         (dict(Y=FAKE + 2, out_f32=1), ALN), (dict(workspace=FAKE + 128), ALN)],
     "hqq_adapters_backward": [
-        (dict(dtype=2), UNS), (dict(M=4000001), INV), (dict(K=4), UNS), (dict(rank=7), UNS),
+        (dict(dtype=2), UNS), (dict(M=2000001), INV), (dict(K=4), UNS), (dict(rank=7), UNS),
         (dict(adapters=1025), UNS), (dict(dY=0), INV), (dict(X=0), INV), (dict(dX=0), INV),
         (dict(dA_f32=0), INV), (dict(dB_f32=0), INV), (dict(workspace=0), INV),
         (dict(M=0, dB_f32=0), INV), (dict(base=FAKE, out_f32=1), INV), (dict(dY=FAKE + 1), ALN),
