@@ -25,6 +25,7 @@ HEADERS = [os.path.join(CSRC, "hqq_internal.h"), os.path.join(CSRC, "hqq_solver.
            os.path.join(CSRC, "hqq_matmul_kernels.h"), os.path.join(CSRC, "hqq_codes.h"),
            os.path.join(CSRC, "hqq_tiles.h"), os.path.join(CSRC, "hqq_matmul_t.h"),
            os.path.join(CSRC, "hqq_adapters.h"), os.path.join(CSRC, "hqq_group_gemm.h"),
+           os.path.join(CSRC, "hqq_low_tile.h"),
            os.path.join(CSRC, "hqq_route.h"),
            os.path.join(CSRC, "hqq_lowrank.h"),
            os.path.join(ROOT, "include", "hqq.h")]

@@ -36,7 +36,7 @@ struct MatmulParams;
 int64_t matmul_adapters_workspace_bytes(const MatmulParams& q, const AdapterParams& p);
 int64_t matmul_adapters_backward_workspace_bytes(const MatmulParams& q, const AdapterParams& p);
 hipError_t launch_matmul_adapters(MatmulParams q, AdapterParams p, int cus, hipStream_t stream);
-hipError_t launch_matmul_adapters_backward(const MatmulParams& q, AdapterParams p, hipStream_t stream);
+hipError_t launch_matmul_adapters_backward(const MatmulParams& q, const AdapterParams& p, hipStream_t stream);
 
 int64_t adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters);
 int64_t adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int rank, int adapters);

@@ -819,8 +819,10 @@ hipError_t launch_forward(const AdapterParams& p, hipStream_t st) {
                            p.adapters, p.base_f32, p.out_f32}, st);
 }
 
+// `t` null: dX is base + the low-rank product; else the weight's product `t` makes it with the low-rank
+// product added (binary16).
 template <typename D>
-hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
+hipError_t launch_backward(const AdapterParams& p, MatmulTParams* t, hipStream_t st) {
   Layout l{static_cast<char*>(p.workspace)};
   const BackwardPlan w(l, p.M, p.N, p.K, p.rank, p.adapters);
   hipError_t e = launch_route_sort(p.ids, p.M, p.adapters, w.s.order, w.s.position, w.s.offsets, w.s.sort_ws, st);
@@ -828,10 +830,10 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
   if (p.M > 0) {
     const auto tiles = [](int64_t n) { return (n + kTransTile - 1) / kTransTile; };
     const int64_t of_a = tiles(p.rank) * tiles(p.K), of_b = tiles(w.Np) * tiles(p.rank);
-    TransposeParams t = {p.A, w.At, p.B, w.Bt, w.s.offsets, p.N, p.K, w.Np, p.rank, p.adapters};
+    TransposeParams tr = {p.A, w.At, p.B, w.Bt, w.s.offsets, p.N, p.K, w.Np, p.rank, p.adapters};
     const int64_t most = of_a > of_b ? of_a : of_b;
     hipLaunchKernelGGL(hqq_adapter_transpose_kernel, dim3((unsigned)(most > 0 ? most : 1), (unsigned)p.adapters, 2),
-                       dim3(kBlock), 0, st, t);
+                       dim3(kBlock), 0, st, tr);
     ShrinkParams s = {};
     s.side[0] = {p.X, p.A, p.K, p.K, w.s.v, D::kScaled ? w.largest[1] : nullptr};
     s.side[1] = {p.dY, w.Bt, p.N, w.Np, w.u, D::kScaled ? w.largest[0] : nullptr};
@@ -858,8 +860,13 @@ hipError_t launch_backward(const AdapterParams& p, hipStream_t st) {
     // right behind the first step, while the cache may still hold the rows it read
     e = launch_outer<D>(o, st);
     if (e != hipSuccess) return e;
-    e = launch_expand<D>({w.u, w.At, p.scales, w.s.order, w.s.offsets, p.base, p.out, p.M, p.K, p.rank,
-                          p.adapters, p.base_f32, p.out_f32}, st);
+    if (t) {
+      t->low = {w.u, w.At, p.scales, p.ids, w.s.order, w.s.offsets, p.K, p.rank, p.adapters};
+      e = launch_matmul_t(*t, st);
+    } else {
+      e = launch_expand<D>({w.u, w.At, p.scales, w.s.order, w.s.offsets, p.base, p.out, p.M, p.K, p.rank,
+                            p.adapters, p.base_f32, p.out_f32}, st);
+    }
     if (e != hipSuccess) return e;
   }
   const int64_t most_elems = (p.N > p.K ? p.N : p.K) * p.rank;
@@ -889,11 +896,11 @@ hipError_t launch_adapters(const AdapterParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_adapters_backward(const AdapterParams& p, hipStream_t stream) {
-  return p.dtype == 0 ? launch_backward<F16>(p, stream) : launch_backward<Bf16>(p, stream);
+  return p.dtype == 0 ? launch_backward<F16>(p, nullptr, stream) : launch_backward<Bf16>(p, nullptr, stream);
 }
 
 // The workspace of a projection with adapters: the adapters' own, then the base in fp32 and the
-// product's workspace (few rows), or the base in fp32 and its workspace (backward).
+// product's workspace (few rows), or the tiles' (more rows, backward).
 int64_t matmul_adapters_workspace_bytes(const MatmulParams& q, const AdapterParams& p) {
   const int64_t own = adapters_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters);
   if (p.M > kFewRows) return own + group_gemm_workspace_bytes(p.M, p.N, p.K, p.adapters, true);
@@ -925,11 +932,7 @@ hipError_t launch_matmul_adapters(MatmulParams q, AdapterParams p, int cus, hipS
     g.order = w.order;
     g.groups = p.adapters;
     g.topk = 1;
-    g.low = w.v;
-    g.factor = p.B;
-    g.scales = p.scales;
-    g.ids = p.ids;
-    g.rank = p.rank;
+    g.low = {w.v, p.B, p.scales, p.ids, w.order, w.offsets, p.N, p.rank, p.adapters};
     g.slabs = l.take<float>(0);
     return launch_group_gemm(g, st);
   }
@@ -964,33 +967,26 @@ hipError_t launch_matmul_adapters(MatmulParams q, AdapterParams p, int cus, hipS
 
 int64_t matmul_adapters_backward_workspace_bytes(const MatmulParams& q, const AdapterParams& p) {
   return adapters_backward_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters) +
-         up256(p.M * p.K * (int64_t)sizeof(float)) + up256(matmul_t_workspace_bytes(p.M, p.N, p.K, 0));
+         up256(matmul_t_workspace_bytes(p.M, p.N, p.K, 0));
 }
 
-hipError_t launch_matmul_adapters_backward(const MatmulParams& q, AdapterParams p, hipStream_t st) {
-  Layout l{static_cast<char*>(p.workspace) + adapters_backward_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters)};
-  float* base = l.take<float>(p.M * p.K);
-  if (p.M > 0) {
-    MatmulTParams t = {};
-    t.dY = p.dY;
-    t.packed = q.packed;
-    t.scale16 = q.scale16;
-    t.zero16 = q.zero16;
-    t.dX = base;
-    t.M = p.M;
-    t.N = p.N;
-    t.K = p.K;
-    t.nbits = q.nbits;
-    t.group_size = q.group_size;
-    t.group_shift = q.group_shift;
-    t.out_f32 = 1;
-    t.slabs = l.take<float>(0);
-    const hipError_t e = launch_matmul_t(t, st);
-    if (e != hipSuccess) return e;
-    p.base = base;
-    p.base_f32 = 1;
-  }
-  return launch_adapters_backward(p, st);
+hipError_t launch_matmul_adapters_backward(const MatmulParams& q, const AdapterParams& p, hipStream_t st) {
+  MatmulTParams t = {};
+  t.dY = p.dY;
+  t.packed = q.packed;
+  t.scale16 = q.scale16;
+  t.zero16 = q.zero16;
+  t.dX = p.out;
+  t.M = p.M;
+  t.N = p.N;
+  t.K = p.K;
+  t.nbits = q.nbits;
+  t.group_size = q.group_size;
+  t.group_shift = q.group_shift;
+  t.out_f32 = p.out_f32;
+  t.slabs = reinterpret_cast<float*>(static_cast<char*>(p.workspace) +
+                                     adapters_backward_workspace_bytes(p.M, p.N, p.K, p.rank, p.adapters));
+  return launch_backward<F16>(p, &t, st);
 }
 
 }  // namespace hqq

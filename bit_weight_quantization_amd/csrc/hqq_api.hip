@@ -638,7 +638,7 @@ int matmul_backward(const void* dY, int64_t M, int64_t N, const void* offsets, i
     if (!workspace) return HQQ_ERR_INVALID_ARG;
     if (!aligned(workspace, 16)) return HQQ_ERR_ALIGNMENT;
   }
-  hqq::MatmulTParams p;
+  hqq::MatmulTParams p = {};
   p.dY = static_cast<const uint16_t*>(dY);
   p.packed = static_cast<const uint8_t*>(packed);
   p.scale16 = static_cast<const uint16_t*>(scale);

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "hqq_low_tile.h"
+
 namespace hqq {
 
 struct GroupGemmParams {
@@ -18,20 +20,14 @@ struct GroupGemmParams {
   const int32_t* order;     // experts: null, or row i is X[order[i] / topk]; adapters: row of X and Y
   const int32_t* offsets;   // first sorted row of every group, groups + 1 values
   int groups, topk;
-  // adapters (low != null): all rows multiply with the one weight, and row i of group g gets
-  // scales[g] low[i] factor[g]^T added
-  const float* low;         // M x rank, sorted
-  const uint16_t* factor;   // groups x N x rank
-  const float* scales;
-  const int32_t* ids;       // group of every row of X (outside [0, groups): none)
-  int rank;
+  LowRank low;              // adapters (low.low set): all rows multiply with the one weight
   float* slabs;             // group_gemm_workspace_bytes(...) bytes
   int xcd_slabs;            // slabs of an XCD (set by the launcher)
 };
 
 int64_t group_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, bool adapters);
 
-// experts x N x K weights (p.low null), or one weight and adapters.
+// experts x N x K weights (p.low.low null), or one weight and adapters.
 hipError_t launch_group_gemm(GroupGemmParams p, hipStream_t stream);
 
 }  // namespace hqq

@@ -40,7 +40,6 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
   constexpr int T = kGWaves * kWave;
   constexpr int XP = BM * kGK / 8 / T;      // 16-byte pieces of X per thread and step
   constexpr int XT = T / (kGK / 8);         // rows of X per round of loads
-  constexpr int RC = 64;                    // low-rank values per round (adapters)
   static_assert(XP >= 1 && XP * T * 8 == BM * kGK && 4 * TJ % TI == 0, "a piece per thread at least, decoding in whole pairs");
   constexpr int BN = 32 * TJ * kGWaves;     // weight rows: one per thread
   static_assert(BN == T, "a thread loads the scales of one weight row");
@@ -265,105 +264,14 @@ if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
 #pragma unroll
   for (int a = 0; a < TI; ++a) back[a] = 1.f;
   if constexpr (ADAPTERS) {
-    // The low-rank products join the same accumulators: s low[m] enters as two binary16 parts of
-    // the row scaled by a power of two (22 bits below the row's largest value), the accumulators of
-    // the row are scaled alike (exact) and scaled back below.  A tile may hold rows of several
-    // adapters: each in turn, with the parts of the other rows left out.
-    const int none_from = P.offsets[P.groups];  // rows of no adapter are behind all others
-    if (place.part == 0 && t.row0 < none_from) {
+    static_assert(low_halves(BM) <= 2 * BM * kGRow, "the parts fit the X buffers");
+    if (place.part == 0) {
       __shared__ float scale_up[BM];
       __shared__ int row_group[BM];
-      _Float16* parts = &As[0][0][0];  // [2][BM][RC + 8]: as large as the X buffers
+      int64_t col[TJ];
 #pragma unroll
-      for (int p = 0; p < XP; ++p) {  // 8 threads share a row
-        const int m = xr + XT * p;
-        int g = -1;
-        if (m < t.rows) {
-          const int32_t o = P.order[t.row0 + m];
-          g = o < 0 ? -1 : P.ids[o];
-        }
-        float largest = 0.f;
-        if (g >= 0)
-          for (int r = xp; r < P.rank; r += 8) {
-            const float v = P.scales[g] * P.low[(t.row0 + m) * P.rank + r];
-            largest = __builtin_isfinite(v) ? __builtin_fmaxf(largest, __builtin_fabsf(v)) : largest;
-          }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) largest = __builtin_fmaxf(largest, __shfl_xor(largest, o, kWave));
-        // 2^x: the largest comes to [2^13, 2^14); x within -114 .. 40, so that the accumulators stay
-        // finite (smaller rows then lose what lies below 2^-64)
-        int x = 13 - ((int)((__builtin_bit_cast(uint32_t, largest) >> 23) & 255) - 127);
-        x = x > 40 ? 40 : x < -114 ? -114 : x;
-        if (xp == 0) {
-          scale_up[m] = g >= 0 ? __builtin_bit_cast(float, (uint32_t)(127 + x) << 23) : 1.f;
-          row_group[m] = g;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int a = 0; a < TI; ++a) {
-        const float up = scale_up[32 * a + i];
-        back[a] = __builtin_bit_cast(float, (uint32_t)(254 << 23) - __builtin_bit_cast(uint32_t, up));  // 1 / up
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[a][j][v] *= up;
-      }
-      for (int m0 = 0; m0 < t.rows;) {  // uniform: the tile's adapters
-        const int g = __builtin_amdgcn_readfirstlane(row_group[m0]);
-        if (g < 0) break;
-        const int64_t gend = P.offsets[g + 1] - t.row0;
-        const int m1 = gend <= m0 ? m0 + 1 : gend < t.rows ? (int)gend : t.rows;  // (past m0 in any case)
-        const float s = P.scales[g];
-        for (int r0 = 0; r0 < P.rank; r0 += RC) {
-          // thread: rows xr + XT p, low-rank values 8 xp .. + 8 of the round
-#pragma unroll
-          for (int p = 0; p < XP; ++p) {
-            const int m = xr + XT * p, r = r0 + 8 * xp;
-            half8_t hi = {}, lo = {};
-            if (m >= m0 && m < m1 && r < P.rank) {
-              const float up = s * scale_up[m];
-              const float* low = P.low + (t.row0 + m) * P.rank + r;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float v = up * low[e];
-                hi[e] = (_Float16)v;
-                lo[e] = __builtin_isfinite((float)hi[e]) ? (_Float16)(v - (float)hi[e]) : (_Float16)0.f;
-              }
-            }
-            *reinterpret_cast<half8_t*>(parts + m * kGRow + 8 * xp) = hi;
-            *reinterpret_cast<half8_t*>(parts + (BM + m) * kGRow + 8 * xp) = lo;
-          }
-          __syncthreads();
-#pragma unroll 1
-          for (int st = 0; st < RC / 16; ++st) {
-            const int r = r0 + 16 * st + 8 * h;
-            if (r0 + 16 * st >= P.rank) break;  // uniform
-            half8_t wl[TJ];
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-              const int64_t n = n0 + 16 * TJ * ((i >> 2) & 1) + 16 * j + 4 * (i >> 3) + (i & 3);
-              wl[j] = (half8_t){};
-              if (n < P.N && r < P.rank)
-                wl[j] = *reinterpret_cast<const half8_t*>(P.factor + ((int64_t)g * P.N + n) * P.rank + r);
-            }
-#pragma unroll
-            for (int a = 0; a < TI; ++a) {
-              if (32 * a >= m1 || 32 * a + 32 <= m0) continue;  // uniform: no row of this adapter
-              const _Float16* src = parts + (32 * a + i) * kGRow + 16 * st + 8 * h;
-              const half8_t hi = *reinterpret_cast<const half8_t*>(src);
-              const half8_t lo = *reinterpret_cast<const half8_t*>(src + BM * kGRow);
-#pragma unroll
-              for (int j = 0; j < TJ; ++j) {
-                acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], hi, acc[a][j], 0, 0, 0);
-                acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], lo, acc[a][j], 0, 0, 0);
-              }
-            }
-          }
-          __syncthreads();
-        }
-        m0 = m1;
-      }
+      for (int j = 0; j < TJ; ++j) col[j] = n0 + 16 * TJ * ((i >> 2) & 1) + 16 * j + 4 * (i >> 3) + (i & 3);
+      add_low<BM, T>(acc, back, P.low, t.row0, t.rows, 0, col, &As[0][0][0], scale_up, row_group);
     }
   }
 
@@ -491,7 +399,7 @@ hipError_t launch_tile(GroupGemmParams p, hipStream_t st) {
 
 template <int NB>
 hipError_t launch_nb(const GroupGemmParams& p, hipStream_t st) {
-  if (p.low) return launch_tile<NB, 4, true>(p, st);
+  if (p.low.low) return launch_tile<NB, 4, true>(p, st);
   return tall_tiles(p.M, p.groups) ? launch_tile<NB, 4, false>(p, st) : launch_tile<NB, 2, false>(p, st);
 }
 

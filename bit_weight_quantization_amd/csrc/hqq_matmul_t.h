@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "hqq_low_tile.h"
+
 namespace hqq {
 
 struct MatmulTParams {
@@ -17,6 +19,7 @@ struct MatmulTParams {
   int out_f32;
   const int32_t* offsets;   // rows sorted by expert: first row of each; null: one weight
   int experts;
+  LowRank low;              // adapters (low.low set, offsets null): rows order[i] of dY and dX
   float* slabs;             // matmul_t_workspace_bytes(...) bytes
   int xcd_slabs;            // slabs of an XCD (set by the launcher)
 };

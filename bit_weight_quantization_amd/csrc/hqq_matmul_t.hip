@@ -56,7 +56,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {  // 2-byte aligned, 
 // ahead in registers, LDS double-buffered, one LDS-only barrier per step.  The weight is the A
 // operand and its row 8 a + 4 h + b stands for column 16 h + 4 a + b of the 32, so that a lane ends
 // with 16 consecutive columns of one row of dX.
-template <int NB, int WM, bool GROUPED>
+enum Rows : int { kAll = 0, kExperts = 1, kAdapted = 2 };  // rows of one weight, of experts, with adapters
+
+template <int NB, int WM, int ROWS>
 __global__ __launch_bounds__(2 * WM * kWave) __attribute__((amdgpu_waves_per_eu(2)))
 void hqq_matmul_t_kernel(const MatmulTParams P) {
   constexpr int T = 2 * WM * kWave, BM = 64 * WM;
@@ -71,14 +73,14 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
 
   const int64_t cols = (P.K + kTK - 1) / kTK;
   const int units = (int)((P.N + kTN * kTUnit - 1) / (kTN * kTUnit));
-  const int64_t tiles = GROUPED ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
+  const int64_t tiles = ROWS == kExperts ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
   const TilePlace place = place_tile(blockIdx.x, tiles, cols, units, t_slots(WM), P.xcd_slabs);
   if (place.tile < 0) return;
   int64_t row0 = place.tile * BM;
   int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);
   int64_t w0 = 0;                    // first weight row of the expert
   int64_t N = P.N;
-  if constexpr (GROUPED) {
+  if constexpr (ROWS == kExperts) {
     const RowTile t = find_row_tile(P.offsets, P.experts, P.M, BM, place.tile);
     if (t.rows <= 0) return;
     row0 = t.row0;
@@ -97,7 +99,12 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int m = xr + T / 8 * i;
-    yrow[i] = P.dY + (row0 + (m < rows ? m : rows - 1)) * P.N + 8 * xp;
+    int64_t row = row0 + (m < rows ? m : rows - 1);
+    if constexpr (ROWS == kAdapted) {
+      const int32_t o = P.low.order[row];
+      row = o < 0 ? ~o : o;
+    }
+    yrow[i] = P.dY + row * P.N + 8 * xp;
   }
   const int br = tid / BP, bp = tid % BP;
   const int64_t kc = k0 + CB * bp < P.K ? k0 + CB * bp : 0;  // (columns past K are not stored)
@@ -213,6 +220,20 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
     }
   }
 
+  float back[2] = {1.f, 1.f};
+  if constexpr (ROWS == kAdapted) {
+    static_assert(low_halves(BM) <= 2 * BM * kTRowA, "the parts fit the buffers of dY");
+    if (place.part == 0) {
+      __shared__ float scale_up[BM];
+      __shared__ int row_group[BM];
+      const int l = lane & 31;
+      int64_t col[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) col[j] = k0 + wn * 64 + j * 32 + 16 * ((l >> 2) & 1) + 4 * (l >> 3) + (l & 3);
+      add_low<BM, T>(acc, back, P.low, row0, rows, wm * 64, col, &As[0][0][0], scale_up, row_group);
+    }
+  }
+
   // lane: row lane % 32 of fragment i, columns 32 j + 16 (lane / 32) .. + 16 (K is a multiple of 32)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -222,13 +243,18 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
       const int c = wn * 64 + j * 32 + 16 * (lane >> 5);
       float v[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
+      for (int e = 0; e < 16; ++e) v[e] = back[i] * acc[i][j][e];
       if (place.parts > 1) {  // a part of the sum, in the block's own slab
         __builtin_memcpy(P.slabs + ((int64_t)place.slot * BM + m) * kTK + c, v, 64);
         continue;
       }
       if (m >= rows || k0 + c >= P.K) continue;
-      const int64_t at = (row0 + m) * P.K + k0 + c;
+      int64_t row = row0 + m;
+      if constexpr (ROWS == kAdapted) {
+        const int32_t o = P.low.order[row];
+        row = o < 0 ? ~o : o;
+      }
+      const int64_t at = row * P.K + k0 + c;
       if (P.out_f32) {
         __builtin_memcpy(static_cast<float*>(P.dX) + at, v, 64);
       } else {
@@ -243,18 +269,18 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
 
 // Tiles that were split: the sum of their parts in order.  A block per split tile and 8 rows.
 constexpr int kTJoinRows = 8;
-template <int WM, bool GROUPED>
+template <int WM, int ROWS>
 __global__ __launch_bounds__(kBlock) void hqq_matmul_t_join_kernel(const MatmulTParams P) {
   constexpr int BM = 64 * WM;
   const int64_t cols = (P.K + kTK - 1) / kTK;
-  const int64_t tiles = GROUPED ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
+  const int64_t tiles = ROWS == kExperts ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
   const int xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
   const TileShare s = tile_share(xcd, tiles * cols, (int)((P.N + kTN * kTUnit - 1) / (kTN * kTUnit)), t_slots(WM));
   if (rest >= s.rest) return;
   const TilePlace place = place_at(s.first + s.full + rest, tiles, cols);
   int64_t row0 = place.tile * BM;
   int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);
-  if constexpr (GROUPED) {
+  if constexpr (ROWS == kExperts) {
     const RowTile t = find_row_tile(P.offsets, P.experts, P.M, BM, place.tile);
     row0 = t.row0;
     rows = t.rows;
@@ -274,7 +300,12 @@ __global__ __launch_bounds__(kBlock) void hqq_matmul_t_join_kernel(const MatmulT
     float y = part[0];
 #pragma unroll
     for (int p = 1; p < kMaxParts; ++p) y += part[p];
-    const int64_t at = (row0 + m) * P.K + k;
+    int64_t row = row0 + m;
+    if constexpr (ROWS == kAdapted) {
+      const int32_t o = P.low.order[row];
+      row = o < 0 ? ~o : o;
+    }
+    const int64_t at = row * P.K + k;
     if (P.out_f32) static_cast<float*>(P.dX)[at] = y;
     else static_cast<_Float16*>(P.dX)[at] = (_Float16)y;
   }
@@ -295,24 +326,25 @@ bool t_splits(int64_t M, int64_t N, int64_t K, int64_t experts, int wm) {
   return experts > 0 || place_splits(t_most(M, K, 0, 64 * wm), (int)(units < kMaxParts ? units : kMaxParts), t_slots(wm));
 }
 
-template <int NB, int WM, bool GROUPED>
+template <int NB, int WM, int ROWS>
 hipError_t launch_t(MatmulTParams P, hipStream_t st) {
-  const int64_t most = t_most(P.M, P.K, GROUPED ? P.experts : 0, 64 * WM), blocks = place_blocks(most, t_slots(WM));
+  const int64_t most = t_most(P.M, P.K, ROWS == kExperts ? P.experts : 0, 64 * WM), blocks = place_blocks(most, t_slots(WM));
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   P.xcd_slabs = place_slabs(most, t_slots(WM));
-  hipLaunchKernelGGL((hqq_matmul_t_kernel<NB, WM, GROUPED>), dim3((unsigned)blocks), dim3(2 * WM * kWave), 0, st, P);
-  if (t_splits(P.M, P.N, P.K, GROUPED ? P.experts : 0, WM)) {  // (split tiles: at most half of an XCD's slots)
+  hipLaunchKernelGGL((hqq_matmul_t_kernel<NB, WM, ROWS>), dim3((unsigned)blocks), dim3(2 * WM * kWave), 0, st, P);
+  if (t_splits(P.M, P.N, P.K, ROWS == kExperts ? P.experts : 0, WM)) {  // (split tiles: at most half of an XCD's slots)
     const dim3 join(kXcds * t_slots(WM) / 2, 64 * WM / kTJoinRows);
-    hipLaunchKernelGGL((hqq_matmul_t_join_kernel<WM, GROUPED>), join, dim3(kBlock), 0, st, P);
+    hipLaunchKernelGGL((hqq_matmul_t_join_kernel<WM, ROWS>), join, dim3(kBlock), 0, st, P);
   }
   return hipGetLastError();
 }
 
 template <int NB>
 hipError_t launch_t_nb(const MatmulTParams& P, hipStream_t st) {
-  if (t_wm(P.M, P.offsets ? P.experts : 0) == 4)
-    return P.offsets ? launch_t<NB, 4, true>(P, st) : launch_t<NB, 4, false>(P, st);
-  return P.offsets ? launch_t<NB, 2, true>(P, st) : launch_t<NB, 2, false>(P, st);
+  const bool tall = t_wm(P.M, P.offsets ? P.experts : 0) == 4;
+  if (P.offsets) return tall ? launch_t<NB, 4, kExperts>(P, st) : launch_t<NB, 2, kExperts>(P, st);
+  if (P.low.low) return tall ? launch_t<NB, 4, kAdapted>(P, st) : launch_t<NB, 2, kAdapted>(P, st);
+  return tall ? launch_t<NB, 4, kAll>(P, st) : launch_t<NB, 2, kAll>(P, st);
 }
 
 }  // namespace

@@ -626,8 +626,9 @@ int64_t hqq_matmul_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int
                                             int group_size, int rank, int adapters);
 
 /*
- * hqq_matmul_adapters_backward -- the gradients of hqq_matmul_adapters for a frozen weight:
- * hqq_matmul_backward in fp32 as the base of hqq_adapters_backward.
+ * hqq_matmul_adapters_backward -- the gradients of hqq_matmul_adapters for a frozen weight: dA and
+ * dB as hqq_adapters_backward, and dX as hqq_matmul_backward with the adapters' part added in its
+ * accumulators (B_a^T dY[m] as two binary16 parts), rounded once.
  * workspace    hqq_matmul_adapters_backward_workspace_bytes(...) bytes, 256-byte aligned.
  */
 int hqq_matmul_adapters_backward(const void* dY_f16, const void* X_f16, int64_t M, int64_t K,
