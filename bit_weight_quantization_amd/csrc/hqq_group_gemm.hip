@@ -386,7 +386,7 @@ template <int NB, int TI, bool ADAPTERS>
 hipError_t launch_tile(GroupGemmParams p, hipStream_t st) {
   const int64_t most = most_tiles(p.M, p.N, p.groups, ADAPTERS, 32 * TI), blocks = place_blocks(most, kGSlots);
   p.xcd_slabs = place_slabs(most, kGSlots);
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (blocks * kGWaves * kWave > UINT32_MAX) return hipErrorInvalidValue;  // threads of a grid
   const dim3 grid((unsigned)blocks), block(kGWaves * kWave);
   if (p.group_shift == 4) hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, true, ADAPTERS>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((hqq_group_gemm_kernel<NB, TI, 2, false, ADAPTERS>), grid, block, 0, st, p);

@@ -329,7 +329,7 @@ bool t_splits(int64_t M, int64_t N, int64_t K, int64_t experts, int wm) {
 template <int NB, int WM, int ROWS>
 hipError_t launch_t(MatmulTParams P, hipStream_t st) {
   const int64_t most = t_most(P.M, P.K, ROWS == kExperts ? P.experts : 0, 64 * WM), blocks = place_blocks(most, t_slots(WM));
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (blocks * 2 * WM * kWave > UINT32_MAX) return hipErrorInvalidValue;  // threads of a grid
   P.xcd_slabs = place_slabs(most, t_slots(WM));
   hipLaunchKernelGGL((hqq_matmul_t_kernel<NB, WM, ROWS>), dim3((unsigned)blocks), dim3(2 * WM * kWave), 0, st, P);
   if (t_splits(P.M, P.N, P.K, ROWS == kExperts ? P.experts : 0, WM)) {  // (split tiles: at most half of an XCD's slots)

@@ -190,18 +190,19 @@ template <typename D, bool WIDE>
 __global__ __launch_bounds__(kBlock) void hqq_route_gather_kernel(const RouteRows P) {
   using T = typename D::T;
   using C = Chunk<D, WIDE>;
-  const int64_t t = blockIdx.x;
-  const T* in = static_cast<const T*>(P.in) + t * P.width;
   T* out = static_cast<T*>(P.out);
-  const int32_t* pos = P.position + t * P.topk;
-  for (int64_t c = (int64_t)threadIdx.x * C::V; c < P.width; c += (int64_t)blockDim.x * C::V) {
-    C x, zero;
-    x.load(in + c);
-    zero.v = (typename C::vec)(T)0;
-    for (int j = 0; j < P.topk; ++j) {
-      const int32_t p = pos[j];
-      if (p >= 0) x.store(out + p * P.width + c);
-      else zero.store(out + (int64_t)~p * P.width + c);  // a dropped slot's row
+  for (int64_t t = blockIdx.x; t < P.tokens; t += gridDim.x) {
+    const T* in = static_cast<const T*>(P.in) + t * P.width;
+    const int32_t* pos = P.position + t * P.topk;
+    for (int64_t c = (int64_t)threadIdx.x * C::V; c < P.width; c += (int64_t)blockDim.x * C::V) {
+      C x, zero;
+      x.load(in + c);
+      zero.v = (typename C::vec)(T)0;
+      for (int j = 0; j < P.topk; ++j) {
+        const int32_t p = pos[j];
+        if (p >= 0) x.store(out + p * P.width + c);
+        else zero.store(out + (int64_t)~p * P.width + c);  // a dropped slot's row
+      }
     }
   }
 }
@@ -214,37 +215,38 @@ template <typename D, bool WIDE>
 __global__ __launch_bounds__(kBlock) void hqq_route_combine_kernel(const RouteRows P) {
   using T = typename D::T;
   using C = Chunk<D, WIDE>;
-  const int64_t t = blockIdx.x;
-  const T* in = static_cast<const T*>(P.in);
-  T* out = static_cast<T*>(P.out) + t * P.width;
-  const int32_t* pos = P.position + t * P.topk;
-  const float* w = P.weights ? P.weights + t * P.topk : nullptr;
-  for (int64_t c = (int64_t)threadIdx.x * C::V; c < P.width; c += (int64_t)blockDim.x * C::V) {
-    float acc[C::V];
+  for (int64_t t = blockIdx.x; t < P.tokens; t += gridDim.x) {
+    const T* in = static_cast<const T*>(P.in);
+    T* out = static_cast<T*>(P.out) + t * P.width;
+    const int32_t* pos = P.position + t * P.topk;
+    const float* w = P.weights ? P.weights + t * P.topk : nullptr;
+    for (int64_t c = (int64_t)threadIdx.x * C::V; c < P.width; c += (int64_t)blockDim.x * C::V) {
+      float acc[C::V];
 #pragma unroll
-    for (int v = 0; v < C::V; ++v) acc[v] = 0.f;
-    for (int j0 = 0; j0 < P.topk; j0 += kTopkStep) {
-      C x[kTopkStep];
-      int32_t p[kTopkStep];
-      float wt[kTopkStep];
+      for (int v = 0; v < C::V; ++v) acc[v] = 0.f;
+      for (int j0 = 0; j0 < P.topk; j0 += kTopkStep) {
+        C x[kTopkStep];
+        int32_t p[kTopkStep];
+        float wt[kTopkStep];
 #pragma unroll
-      for (int j = 0; j < kTopkStep; ++j) {
-        p[j] = j0 + j < P.topk ? pos[j0 + j] : -1;
-        wt[j] = p[j] >= 0 && w ? w[j0 + j] : 1.f;
-        if (p[j] >= 0) x[j].load(in + p[j] * P.width + c);
-      }
+        for (int j = 0; j < kTopkStep; ++j) {
+          p[j] = j0 + j < P.topk ? pos[j0 + j] : -1;
+          wt[j] = p[j] >= 0 && w ? w[j0 + j] : 1.f;
+          if (p[j] >= 0) x[j].load(in + p[j] * P.width + c);
+        }
 #pragma unroll
-      for (int j = 0; j < kTopkStep; ++j) {
-        if (p[j] >= 0) {
+        for (int j = 0; j < kTopkStep; ++j) {
+          if (p[j] >= 0) {
 #pragma unroll
-          for (int v = 0; v < C::V; ++v) acc[v] = __builtin_fmaf(wt[j], D::up(x[j].v[v]), acc[v]);
+            for (int v = 0; v < C::V; ++v) acc[v] = __builtin_fmaf(wt[j], D::up(x[j].v[v]), acc[v]);
+          }
         }
       }
-    }
-    C y;
+      C y;
 #pragma unroll
-    for (int v = 0; v < C::V; ++v) y.v[v] = D::down(acc[v]);
-    y.store(out + c);
+      for (int v = 0; v < C::V; ++v) y.v[v] = D::down(acc[v]);
+      y.store(out + c);
+    }
   }
 }
 
@@ -256,62 +258,63 @@ __global__ __launch_bounds__(kBlock) void hqq_route_combine_backward_kernel(cons
   using T = typename D::T;
   using C = Chunk<D, WIDE>;
   __shared__ float part[kBlock / kWave][kTopkStep];
-  const int64_t t = blockIdx.x;
   const int wid = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
   const int waves = blockDim.x / kWave;
   const T* in = static_cast<const T*>(P.in);
-  const T* grad = static_cast<const T*>(P.grad) + t * P.width;
   T* out = static_cast<T*>(P.out);
-  const int32_t* pos = P.position + t * P.topk;
-  for (int j0 = 0; j0 < P.topk; j0 += kTopkStep) {
-    int32_t p[kTopkStep];
-    float wt[kTopkStep], dot[kTopkStep];
-#pragma unroll
-    for (int j = 0; j < kTopkStep; ++j) {
-      p[j] = j0 + j < P.topk ? pos[j0 + j] : -1;
-      wt[j] = p[j] >= 0 && P.weights ? P.weights[t * P.topk + j0 + j] : 1.f;
-      dot[j] = 0.f;
-    }
-    for (int64_t c = (int64_t)threadIdx.x * C::V; c < P.width; c += (int64_t)blockDim.x * C::V) {
-      C g, x[kTopkStep];
-      g.load(grad + c);
-      if (P.dweights) {
-#pragma unroll
-        for (int j = 0; j < kTopkStep; ++j)
-          if (p[j] >= 0) x[j].load(in + p[j] * P.width + c);
-      }
+  for (int64_t t = blockIdx.x; t < P.tokens; t += gridDim.x) {
+    const T* grad = static_cast<const T*>(P.grad) + t * P.width;
+    const int32_t* pos = P.position + t * P.topk;
+    for (int j0 = 0; j0 < P.topk; j0 += kTopkStep) {
+      int32_t p[kTopkStep];
+      float wt[kTopkStep], dot[kTopkStep];
 #pragma unroll
       for (int j = 0; j < kTopkStep; ++j) {
-        if (j0 + j >= P.topk) continue;
-        C d;
-        if (p[j] >= 0) {
+        p[j] = j0 + j < P.topk ? pos[j0 + j] : -1;
+        wt[j] = p[j] >= 0 && P.weights ? P.weights[t * P.topk + j0 + j] : 1.f;
+        dot[j] = 0.f;
+      }
+      for (int64_t c = (int64_t)threadIdx.x * C::V; c < P.width; c += (int64_t)blockDim.x * C::V) {
+        C g, x[kTopkStep];
+        g.load(grad + c);
+        if (P.dweights) {
 #pragma unroll
-          for (int v = 0; v < C::V; ++v) {
-            const float gv = D::up(g.v[v]);
-            d.v[v] = D::down(wt[j] * gv);
-            if (P.dweights) dot[j] = __builtin_fmaf(gv, D::up(x[j].v[v]), dot[j]);
+          for (int j = 0; j < kTopkStep; ++j)
+            if (p[j] >= 0) x[j].load(in + p[j] * P.width + c);
+        }
+#pragma unroll
+        for (int j = 0; j < kTopkStep; ++j) {
+          if (j0 + j >= P.topk) continue;
+          C d;
+          if (p[j] >= 0) {
+#pragma unroll
+            for (int v = 0; v < C::V; ++v) {
+              const float gv = D::up(g.v[v]);
+              d.v[v] = D::down(wt[j] * gv);
+              if (P.dweights) dot[j] = __builtin_fmaf(gv, D::up(x[j].v[v]), dot[j]);
+            }
+            d.store(out + p[j] * P.width + c);
+          } else {
+            d.v = (typename C::vec)(T)0;
+            d.store(out + (int64_t)~p[j] * P.width + c);
           }
-          d.store(out + p[j] * P.width + c);
-        } else {
-          d.v = (typename C::vec)(T)0;
-          d.store(out + (int64_t)~p[j] * P.width + c);
         }
       }
-    }
-    if (!P.dweights) continue;
+      if (!P.dweights) continue;
 #pragma unroll
-    for (int j = 0; j < kTopkStep; ++j) {
+      for (int j = 0; j < kTopkStep; ++j) {
 #pragma unroll
-      for (int o = kWave / 2; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o, kWave);
-      if (lane == 0) part[wid][j] = dot[j];
+        for (int o = kWave / 2; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o, kWave);
+        if (lane == 0) part[wid][j] = dot[j];
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < kTopkStep && j0 + (int)threadIdx.x < P.topk) {
+        float sum = 0.f;
+        for (int w = 0; w < waves; ++w) sum += part[w][threadIdx.x];
+        P.dweights[t * P.topk + j0 + threadIdx.x] = sum;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if ((int)threadIdx.x < kTopkStep && j0 + (int)threadIdx.x < P.topk) {
-      float sum = 0.f;
-      for (int w = 0; w < waves; ++w) sum += part[w][threadIdx.x];
-      P.dweights[t * P.topk + j0 + threadIdx.x] = sum;
-    }
-    __syncthreads();
   }
 }
 
@@ -329,11 +332,14 @@ int row_threads(int64_t width, int v) {
   return chunks <= kWave ? kWave : (int)((chunks + kWave - 1) / kWave) * kWave;
 }
 
+constexpr int64_t kRowBlocks = 1 << 22;
+
 enum class Rows { kGather, kCombine, kBackward };
 
 template <typename D, bool WIDE>
 hipError_t launch_rows(const RouteRows& p, Rows what, hipStream_t st) {
-  const dim3 grid((unsigned)p.tokens), block(row_threads(p.width, Chunk<D, WIDE>::V));
+  // (a grid may have 2^32 threads; blocks go on to further tokens)
+  const dim3 grid((unsigned)(p.tokens < kRowBlocks ? p.tokens : kRowBlocks)), block(row_threads(p.width, Chunk<D, WIDE>::V));
   switch (what) {
     case Rows::kGather: hipLaunchKernelGGL((hqq_route_gather_kernel<D, WIDE>), grid, block, 0, st, p); break;
     case Rows::kCombine: hipLaunchKernelGGL((hqq_route_combine_kernel<D, WIDE>), grid, block, 0, st, p); break;

@@ -157,6 +157,21 @@ def test_rows_of_any_alignment(hq):
         assert torch.equal(back, (X.float() * n[:, None]).half())
 
 
+def test_more_tokens_than_one_grid_has_threads_for(hq):
+    """70 million tokens of one element (64 threads each would be 4.5e9): blocks take several."""
+    T = 70_000_000
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    ids[1::2] = 1
+    r = hq.expert_sort(ids, 2)
+    assert r.offsets.tolist() == [0, T // 2, T]
+    X = torch.arange(T, device="cuda", dtype=torch.int32).remainder_(2039).half()[:, None]
+    Xs = hq.expert_gather(X, r)
+    assert torch.equal(Xs[:T // 2], X[0::2]) and torch.equal(Xs[T // 2:], X[1::2])
+    assert torch.equal(hq.expert_combine(Xs, r), X)
+    dY, none = hq.expert_combine_backward(X, None, r)
+    assert none is None and torch.equal(dY, Xs)
+
+
 def test_combine_gradients_agree_with_differences(hq):
     """combine is linear in the rows and in the weights: on small integers in float32 its exact
     differences equal the gradients' products with the direction."""
