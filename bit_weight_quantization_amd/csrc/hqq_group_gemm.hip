@@ -339,7 +339,7 @@ __global__ __launch_bounds__(64 * kGWaves) void hqq_group_gemm_join_kernel(const
   const int64_t tiles = ADAPTERS ? (P.M + BM - 1) / BM : count_row_tiles(P.offsets, P.groups, P.M, BM);
   const int xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
   const TileShare s = tile_share(xcd, tiles * cols, (int)((P.K + kGUnit - 1) / kGUnit), kGSlots);
-  if (rest >= s.rest) return;
+  if (rest >= s.rest || (rest + 1) * s.parts > P.xcd_slabs) return;
   const TilePlace place = place_at(s.first + s.full + rest, tiles, cols);
   int64_t row0 = place.tile * BM;
   int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);

@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kBlock) void hqq_matmul_t_join_kernel(const MatmulT
   const int64_t tiles = ROWS == kExperts ? count_row_tiles(P.offsets, P.experts, P.M, BM) : (P.M + BM - 1) / BM;
   const int xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
   const TileShare s = tile_share(xcd, tiles * cols, (int)((P.N + kTN * kTUnit - 1) / (kTN * kTUnit)), t_slots(WM));
-  if (rest >= s.rest) return;
+  if (rest >= s.rest || (rest + 1) * s.parts > P.xcd_slabs) return;
   const TilePlace place = place_at(s.first + s.full + rest, tiles, cols);
   int64_t row0 = place.tile * BM;
   int rows = (int)(P.M - row0 < BM ? P.M - row0 : BM);

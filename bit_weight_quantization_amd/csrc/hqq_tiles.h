@@ -83,12 +83,13 @@ __device__ __forceinline__ int64_t count_row_tiles(const int32_t* offsets, int g
 }
 
 // Place of block `id` of a one-dimensional grid among tiles x cols output tiles, for blocks of
-// which an XCD holds `slots` at a time (its 32 CUs times one or two).  Workgroups go to the 8 XCDs (each with an L2 of its own) in turn, so XCD
-// id % 8 takes one contiguous eighth of an order in which 8 row tiles share a column tile before the
-// next one comes: the blocks that run on one XCD at a time then read few distinct tiles of either
-// operand.  The tiles of an XCD's share that would run alone after its last full round are
-// each split over blocks along the inner size (units of it; at most 8 parts), whose partial sums
-// a second kernel adds in order: a round that is not full costs as much time as a full one.
+// which an XCD holds `slots` at a time (its 32 CUs times one or two).  Workgroups go to the 8 XCDs
+// (each with an L2 of its own) in turn, so XCD id % 8 takes one contiguous eighth of an order in
+// which 8 row tiles share a column tile before the next one comes: the blocks that run on one XCD
+// at a time then read few distinct tiles of either operand.  The tiles of an XCD's share that would
+// run alone after its last full round are each split over blocks along the inner size (units of it;
+// at most 8 parts), whose partial sums a second kernel adds in order: a round that is not full
+// costs as much time as a full one.
 constexpr int kXcds = 8, kBand = 8;
 constexpr int kMaxParts = 8;
 
@@ -127,7 +128,8 @@ __device__ __forceinline__ TilePlace place_tile(int64_t id, int64_t tiles, int64
   const int64_t at = id / kXcds;
   if (at < s.full) return place_at(s.first + at, tiles, cols);
   const int64_t p = at - s.full;
-  if (p >= (int64_t)s.rest * s.parts) return {-1, 0, 0, 1, 0};
+  // (the second condition holds whenever offsets ascend; a slab is never outside, whatever is stored)
+  if (p >= (int64_t)s.rest * s.parts || p >= xcd_slabs) return {-1, 0, 0, 1, 0};
   TilePlace t = place_at(s.first + s.full + p / s.parts, tiles, cols);
   t.part = (int)(p % s.parts);
   t.parts = s.parts;
