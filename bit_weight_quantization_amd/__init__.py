@@ -911,9 +911,9 @@ def _scratch(workspace, nbytes: int, device):
         return None
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not workspace.is_cuda or workspace.device != device or \
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError(f"workspace needs {nbytes} bytes of memory of {device}")
+        raise ValueError(f"workspace needs {nbytes} contiguous bytes of memory of {device}")
     return workspace
 
 
@@ -1018,7 +1018,9 @@ def expert_combine_backward(dOut, Ys, route: ExpertOrder, weights=None, stream=N
     dev, width = route.order.device, dOut.shape[1]
     _take(dOut, "dOut", dOut.dtype, (route.tokens, width), dev)
     w = _weights_of(weights, route)
-    if w is not None or Ys is not None:
+    if w is not None and Ys is None:
+        raise ValueError("the weights' gradient needs Ys")
+    if Ys is not None:
         _take(Ys, "Ys", dOut.dtype, (route.rows, width), dev)
 
     def call(sh):

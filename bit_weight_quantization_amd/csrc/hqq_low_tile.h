@@ -121,10 +121,19 @@ __device__ __forceinline__ void add_low(float16_t (&acc)[TA][TJ], float (&back)[
           const _Float16* src = parts + (f + i) * kLowRow + 16 * st + 8 * h;
           const half8_t hi = *reinterpret_cast<const half8_t*>(src);
           const half8_t lo = *reinterpret_cast<const half8_t*>(src + BM * kLowRow);
+          // a lane's sums are one row's: rows of another adapter keep theirs, also where this one's
+          // factor holds an infinity or a NaN (times their zeros)
+          const bool mine = f + i >= m0 && f + i < m1;
 #pragma unroll
           for (int j = 0; j < TJ; ++j) {
-            acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], hi, acc[a][j], 0, 0, 0);
-            acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], lo, acc[a][j], 0, 0, 0);
+            float16_t sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], hi, acc[a][j], 0, 0, 0);
+            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(wl[j], lo, sum, 0, 0, 0);
+            if (f >= m0 && f + 32 <= m1) {  // uniform
+              acc[a][j] = sum;
+            } else {
+#pragma unroll
+              for (int v = 0; v < 16; ++v) acc[a][j][v] = mine ? sum[v] : acc[a][j][v];
+            }
           }
         }
       }

@@ -152,6 +152,35 @@ def test_what_a_row_does_not_use_reaches_no_result(hq, M):
     assert torch.equal(got[2], clean[2]) and torch.equal(got[3], clean[3])
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("M", [2, 5, 64, 65, 300])
+def test_an_adapter_that_holds_nan_spoils_its_own_rows_only(hq, M, dtype):
+    """Other requests' rows, and rows of no adapter, keep their results when one adapter in use (its
+    rows between theirs, in the same tiles) holds NaN and infinities."""
+    N, K = 260, 640
+    t = _adapters(M, N, K, 16, 4, 0.0, seed=M)
+    t["ids"] = torch.arange(M, device="cuda", dtype=torch.int32) % 4 - 1  # -1, 0, 1, 2, -1, ...
+    t = {k: v.to(dtype) if v.dtype == torch.float16 else v for k, v in t.items()}
+    dY = _ints((M, N), seed=M, lim=1).to(dtype)
+    bad = dict(t, A=t["A"].clone(), B=t["B"].clone())
+    bad["A"][0, 3, 5], bad["A"][0, 4, :] = float("inf"), float("nan")
+    bad["B"][0, 7, 2], bad["B"][0, 11, :] = float("nan"), float("-inf")
+    keep, other = t["ids"] != 0, torch.arange(4, device="cuda") != 0
+    calls = [lambda u: (hq.adapters(**u), *hq.adapters_backward(dY, **u))]
+    if dtype == torch.float16:
+        for nbits in (4, 3):
+            q, _ = _quantized(hq, N, K, nbits, 64, seed=8)
+            calls.append(lambda u, q=q: (hq.matmul_adapters(u["X"], q, u["A"], u["B"], u["ids"], u["scales"]),
+                                         *hq.matmul_adapters_backward(dY, u["X"], q, u["A"], u["B"], u["ids"], u["scales"])))
+    for call in calls:
+        clean, got = call(t), call(bad)
+        for a, b in zip(got[:2], clean[:2]):
+            assert torch.equal(a[keep], b[keep])
+        for a, b in zip(got[2:], clean[2:]):
+            assert torch.equal(a[other], b[other])
+        assert not bool(got[0][~keep].isfinite().all(1).any())
+
+
 def test_one_workspace_serves_call_after_call(hq):
     """A workspace that the caller keeps, with what earlier calls of other sizes left in it."""
     held = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")  # NaN in every type
