@@ -42,11 +42,12 @@ EXPORTED_SYMBOLS = ("hqq_quantize", "hqq_quantize_ex", "hqq_quantize_batch", "hq
                     "hqq_matmul_backward", "hqq_matmul_backward_workspace_bytes",
                     "hqq_expert_sort", "hqq_expert_sort_workspace_bytes", "hqq_expert_gather",
                     "hqq_expert_combine", "hqq_expert_combine_backward", "hqq_matmul_experts",
-                    "hqq_matmul_experts_workspace_bytes", "hqq_matmul_experts_backward", "hqq_matmul_experts_backward_workspace_bytes",
-                    "hqq_adapters", "hqq_adapters_workspace_bytes", "hqq_adapters_backward",
-                    "hqq_adapters_backward_workspace_bytes",
-                    "hqq_matmul_adapters", "hqq_matmul_adapters_workspace_bytes",
-                    "hqq_matmul_adapters_backward", "hqq_matmul_adapters_backward_workspace_bytes")
+                    "hqq_matmul_experts_workspace_bytes", "hqq_matmul_experts_backward",
+                    "hqq_matmul_experts_backward_workspace_bytes", "hqq_adapters",
+                    "hqq_adapters_workspace_bytes", "hqq_adapters_backward",
+                    "hqq_adapters_backward_workspace_bytes", "hqq_matmul_adapters",
+                    "hqq_matmul_adapters_workspace_bytes", "hqq_matmul_adapters_backward",
+                    "hqq_matmul_adapters_backward_workspace_bytes")
 
 
 class HQQError(RuntimeError):
@@ -128,11 +129,12 @@ def load_library(path: str = LIB_PATH):
             ("hqq_matmul_experts", [P, I64, I64, P, I, P, I, P, P, P, I64, I, I, P, I, P, P]),
             ("hqq_matmul_experts_backward", [P, I64, I64, P, I, P, P, P, I64, I, I, P, I, P, P]),
             ("hqq_adapters", [P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P]),
-            ("hqq_adapters_backward", [P, P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P, P,
-                                       P]),
-            ("hqq_matmul_adapters", [P, I64, I64, P, P, P, I64, I, I, P, P, I, I, P, P, P, I, P, P]),
-            ("hqq_matmul_adapters_backward", [P, P, I64, I64, P, P, P, I64, I, I, P, P, I, I, P, P, P,
-                                              I, P, P, P, P])):
+            ("hqq_adapters_backward", [P, P, I, I64, I64, P, P, I64, I, I, P, P, P, I, P, I, P, P,
+                                       P, P]),
+            ("hqq_matmul_adapters", [P, I64, I64, P, P, P, I64, I, I, P, P, I, I, P, P, P, I, P,
+                                     P]),
+            ("hqq_matmul_adapters_backward", [P, P, I64, I64, P, P, P, I64, I, I, P, P, I, I, P, P,
+                                              P, I, P, P, P, P])):
         getattr(lib, name).restype = I
         getattr(lib, name).argtypes = args
     for name, args in (
@@ -294,8 +296,9 @@ def hqq_dequantize(packed_codes: int, scale_f16: int, zero_f16: int, rows: int, 
 def hqq_matmul_backward(dY_f16: int, M: int, N: int, packed_codes: int, scale_f16: int,
                         zero_f16: int, K: int, nbits: int, group_size: int, dX: int, out_f32: int,
                         workspace: int = 0, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_matmul_backward(dY_f16, M, N, packed_codes, scale_f16, zero_f16, K,
-                                              nbits, group_size, dX, out_f32, workspace, stream)
+    return (_lib or load_library()).hqq_matmul_backward(dY_f16, M, N, packed_codes, scale_f16,
+                                                        zero_f16, K, nbits, group_size, dX, out_f32,
+                                                        workspace, stream)
 
 
 def hqq_matmul_backward_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -305,8 +308,8 @@ def hqq_matmul_backward_workspace_bytes(M: int, N: int, K: int) -> int:
 def hqq_expert_sort(ids_i32: int, tokens: int, topk: int, experts: int, order_i32: int,
                     position_i32: int, offsets_i32: int, workspace: int = 0,
                     stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_expert_sort(ids_i32, tokens, topk, experts, order_i32, position_i32,
-                                          offsets_i32, workspace, stream)
+    return (_lib or load_library()).hqq_expert_sort(ids_i32, tokens, topk, experts, order_i32,
+                                                    position_i32, offsets_i32, workspace, stream)
 
 
 def hqq_expert_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
@@ -315,30 +318,32 @@ def hqq_expert_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int
 
 def hqq_expert_gather(X: int, dtype: int, tokens: int, topk: int, width: int, position_i32: int,
                       Xs: int, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_expert_gather(X, dtype, tokens, topk, width, position_i32, Xs, stream)
+    return (_lib or load_library()).hqq_expert_gather(X, dtype, tokens, topk, width, position_i32,
+                                                      Xs, stream)
 
 
 def hqq_expert_combine(Ys: int, dtype: int, tokens: int, topk: int, width: int, position_i32: int,
                        weights_f32: int, out: int, stream: int = 0) -> int:
     return (_lib or load_library()).hqq_expert_combine(Ys, dtype, tokens, topk, width, position_i32,
-                                             weights_f32, out, stream)
+                                                       weights_f32, out, stream)
 
 
 def hqq_expert_combine_backward(dOut: int, Ys: int, dtype: int, tokens: int, topk: int, width: int,
                                 position_i32: int, weights_f32: int, dYs: int, dweights_f32: int,
                                 stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_expert_combine_backward(dOut, Ys, dtype, tokens, topk, width,
-                                                      position_i32, weights_f32, dYs, dweights_f32,
-                                                      stream)
+    return (_lib or load_library()).hqq_expert_combine_backward(dOut, Ys, dtype, tokens, topk,
+                                                            width, position_i32, weights_f32, dYs,
+                                                            dweights_f32, stream)
 
 
 def hqq_matmul_experts(X_f16: int, rows: int, K: int, order_i32: int, topk: int, offsets_i32: int,
                        experts: int, packed_codes: int, scale_f16: int, zero_f16: int, N: int,
                        nbits: int, group_size: int, Y: int, out_f32: int, workspace: int = 0,
                        stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_matmul_experts(X_f16, rows, K, order_i32, topk, offsets_i32, experts,
-                                             packed_codes, scale_f16, zero_f16, N, nbits,
-                                             group_size, Y, out_f32, workspace, stream)
+    return (_lib or load_library()).hqq_matmul_experts(X_f16, rows, K, order_i32, topk, offsets_i32,
+                                                       experts, packed_codes, scale_f16, zero_f16,
+                                                       N, nbits, group_size, Y, out_f32, workspace,
+                                                       stream)
 
 
 def hqq_matmul_experts_workspace_bytes(rows: int, N: int, K: int, experts: int) -> int:
@@ -349,9 +354,10 @@ def hqq_matmul_experts_backward(dY_f16: int, rows: int, N: int, offsets_i32: int
                                 packed_codes: int, scale_f16: int, zero_f16: int, K: int,
                                 nbits: int, group_size: int, dX: int, out_f32: int,
                                 workspace: int = 0, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_matmul_experts_backward(dY_f16, rows, N, offsets_i32, experts,
-                                                      packed_codes, scale_f16, zero_f16, K, nbits,
-                                                      group_size, dX, out_f32, workspace, stream)
+    return (_lib or load_library()).hqq_matmul_experts_backward(dY_f16, rows, N, offsets_i32,
+                                                            experts, packed_codes, scale_f16,
+                                                            zero_f16, K, nbits, group_size, dX,
+                                                            out_f32, workspace, stream)
 
 
 def hqq_matmul_experts_backward_workspace_bytes(rows: int, N: int, K: int, experts: int) -> int:
@@ -361,8 +367,9 @@ def hqq_matmul_experts_backward_workspace_bytes(rows: int, N: int, K: int, exper
 def hqq_adapters(X: int, dtype: int, M: int, K: int, A: int, B: int, N: int, rank: int,
                  adapters: int, ids_i32: int, scales_f32: int, base: int, base_f32: int, Y: int,
                  out_f32: int, workspace: int, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_adapters(X, dtype, M, K, A, B, N, rank, adapters, ids_i32, scales_f32,
-                                       base, base_f32, Y, out_f32, workspace, stream)
+    return (_lib or load_library()).hqq_adapters(X, dtype, M, K, A, B, N, rank, adapters, ids_i32,
+                                                 scales_f32, base, base_f32, Y, out_f32, workspace,
+                                                 stream)
 
 
 def hqq_adapters_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
@@ -373,9 +380,10 @@ def hqq_adapters_backward(dY: int, X: int, dtype: int, M: int, K: int, A: int, B
                           rank: int, adapters: int, ids_i32: int, scales_f32: int, base: int,
                           base_f32: int, dX: int, out_f32: int, dA_f32: int, dB_f32: int,
                           workspace: int, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_adapters_backward(dY, X, dtype, M, K, A, B, N, rank, adapters, ids_i32,
-                                                scales_f32, base, base_f32, dX, out_f32, dA_f32,
-                                                dB_f32, workspace, stream)
+    return (_lib or load_library()).hqq_adapters_backward(dY, X, dtype, M, K, A, B, N, rank,
+                                                          adapters, ids_i32, scales_f32, base,
+                                                          base_f32, dX, out_f32, dA_f32, dB_f32,
+                                                          workspace, stream)
 
 
 def hqq_adapters_backward_workspace_bytes(M: int, N: int, K: int, rank: int, adapters: int) -> int:
@@ -386,15 +394,16 @@ def hqq_matmul_adapters(X_f16: int, M: int, K: int, packed_codes: int, scale_f16
                         zero_f16: int, N: int, nbits: int, group_size: int, A_f16: int, B_f16: int,
                         rank: int, adapters: int, ids_i32: int, scales_f32: int, Y: int,
                         out_f32: int, workspace: int, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_matmul_adapters(X_f16, M, K, packed_codes, scale_f16, zero_f16, N,
-                                              nbits, group_size, A_f16, B_f16, rank, adapters,
-                                              ids_i32, scales_f32, Y, out_f32, workspace, stream)
+    return (_lib or load_library()).hqq_matmul_adapters(X_f16, M, K, packed_codes, scale_f16,
+                                                        zero_f16, N, nbits, group_size, A_f16,
+                                                        B_f16, rank, adapters, ids_i32, scales_f32,
+                                                        Y, out_f32, workspace, stream)
 
 
 def hqq_matmul_adapters_workspace_bytes(M: int, N: int, K: int, nbits: int, group_size: int,
                                         rank: int, adapters: int) -> int:
-    return (_lib or load_library()).hqq_matmul_adapters_workspace_bytes(M, N, K, nbits, group_size, rank,
-                                                              adapters)
+    return (_lib or load_library()).hqq_matmul_adapters_workspace_bytes(M, N, K, nbits, group_size,
+                                                            rank, adapters)
 
 
 def hqq_matmul_adapters_backward(dY_f16: int, X_f16: int, M: int, K: int, packed_codes: int,
@@ -402,15 +411,18 @@ def hqq_matmul_adapters_backward(dY_f16: int, X_f16: int, M: int, K: int, packed
                                  group_size: int, A_f16: int, B_f16: int, rank: int, adapters: int,
                                  ids_i32: int, scales_f32: int, dX: int, out_f32: int, dA_f32: int,
                                  dB_f32: int, workspace: int, stream: int = 0) -> int:
-    return (_lib or load_library()).hqq_matmul_adapters_backward(
-        dY_f16, X_f16, M, K, packed_codes, scale_f16, zero_f16, N, nbits, group_size, A_f16, B_f16,
-        rank, adapters, ids_i32, scales_f32, dX, out_f32, dA_f32, dB_f32, workspace, stream)
+    return (_lib or load_library()).hqq_matmul_adapters_backward( dY_f16, X_f16, M, K, packed_codes,
+                                                            scale_f16, zero_f16, N, nbits,
+                                                            group_size, A_f16, B_f16, rank,
+                                                            adapters, ids_i32, scales_f32, dX,
+                                                            out_f32, dA_f32, dB_f32, workspace,
+                                                            stream)
 
 
 def hqq_matmul_adapters_backward_workspace_bytes(M: int, N: int, K: int, nbits: int,
                                                  group_size: int, rank: int, adapters: int) -> int:
-    return (_lib or load_library()).hqq_matmul_adapters_backward_workspace_bytes(M, N, K, nbits, group_size,
-                                                                       rank, adapters)
+    return (_lib or load_library()).hqq_matmul_adapters_backward_workspace_bytes(M, N, K, nbits,
+                                                            group_size, rank, adapters)
 
 
 # ----------------------------------------------------------- torch helpers --
@@ -975,7 +987,8 @@ def expert_gather(X, route: ExpertOrder, out=None, stream=None):
     def call(sh):
         y = _result(out, (route.rows, width), X.dtype, dev)
         _check_status(hqq_expert_gather(X.data_ptr(), code, route.tokens, route.topk, width,
-                                        route.position.data_ptr(), y.data_ptr(), sh), "hqq_expert_gather")
+                                        route.position.data_ptr(), y.data_ptr(), sh),
+                                        "hqq_expert_gather")
         return y
     return _launch(dev, stream, call)
 
@@ -1028,8 +1041,9 @@ def expert_combine_backward(dOut, Ys, route: ExpertOrder, weights=None, stream=N
         dw = None if w is None else torch.empty((route.tokens, route.topk), dtype=torch.float32,
                                                 device=dev)
         _check_status(hqq_expert_combine_backward(
-            dOut.data_ptr(), _addr(Ys), code, route.tokens, route.topk, width, route.position.data_ptr(),
-            _addr(w), dYs.data_ptr(), _addr(dw), sh), "hqq_expert_combine_backward")
+            dOut.data_ptr(), _addr(Ys), code, route.tokens, route.topk, width,
+            route.position.data_ptr(), _addr(w), dYs.data_ptr(), _addr(dw), sh),
+            "hqq_expert_combine_backward")
         return dYs, dw
     return _launch(dev, stream, call)
 
@@ -1058,9 +1072,9 @@ def matmul_experts(X, q: "QuantizedWeight", route: ExpertOrder, sorted_rows: boo
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_experts(
             X.data_ptr(), route.rows, K, 0 if sorted_rows else route.order.data_ptr(), route.topk,
-            route.offsets.data_ptr(), route.experts, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N,
-            q.nbits, q.group_size, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh),
-            "hqq_matmul_experts")
+            route.offsets.data_ptr(), route.experts, q.packed.data_ptr(), q.scale.data_ptr(),
+            q.zero.data_ptr(), N, q.nbits, q.group_size, y.data_ptr(), int(bool(out_f32)),
+            _addr(ws), sh), "hqq_matmul_experts")
         return y
     return _launch(dev, stream, call)
 
@@ -1080,9 +1094,9 @@ def matmul_experts_backward(dYs, q: "QuantizedWeight", route: ExpertOrder, out_f
         y = _result(out, (route.rows, K), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_experts_backward(
-            dYs.data_ptr(), route.rows, N, route.offsets.data_ptr(), route.experts, q.packed.data_ptr(),
-            q.scale.data_ptr(), q.zero.data_ptr(), K, q.nbits, q.group_size, y.data_ptr(), int(bool(out_f32)),
-            _addr(ws), sh), "hqq_matmul_experts_backward")
+            dYs.data_ptr(), route.rows, N, route.offsets.data_ptr(), route.experts,
+            q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), K, q.nbits, q.group_size,
+            y.data_ptr(), int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_experts_backward")
         return y
     return _launch(dev, stream, call)
 
@@ -1103,8 +1117,9 @@ def matmul_backward(dY, q: "QuantizedWeight", out_f32: bool = False, out=None, w
         y = _result(out, (M, q.cols), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_backward(
-            dY.data_ptr(), M, q.rows, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), q.cols, q.nbits,
-            q.group_size, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_backward")
+            dY.data_ptr(), M, q.rows, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(),
+            q.cols, q.nbits, q.group_size, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh),
+            "hqq_matmul_backward")
         return y
     return _launch(dev, stream, call)
 
@@ -1147,8 +1162,9 @@ def adapters(X, A, B, ids, scales, base=None, out_f32: bool = False, out=None, w
         y = _result(out, (M, N), torch.float32 if out_f32 else X.dtype, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_adapters(
-            X.data_ptr(), code, M, K, A.data_ptr(), B.data_ptr(), N, rank, n, ids.data_ptr(), scales.data_ptr(),
-            _addr(base), b32, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh), "hqq_adapters")
+            X.data_ptr(), code, M, K, A.data_ptr(), B.data_ptr(), N, rank, n, ids.data_ptr(),
+            scales.data_ptr(), _addr(base), b32, y.data_ptr(), int(bool(out_f32)), _addr(ws), sh),
+            "hqq_adapters")
         return y
     return _launch(dev, stream, call)
 
@@ -1169,9 +1185,9 @@ def adapters_backward(dY, X, A, B, ids, scales, base=None, out_f32: bool = False
         dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_adapters_backward(
-            dY.data_ptr(), X.data_ptr(), code, M, K, A.data_ptr(), B.data_ptr(), N, rank, n, ids.data_ptr(),
-            scales.data_ptr(), _addr(base), b32, dX.data_ptr(), int(bool(out_f32)), dA.data_ptr(), dB.data_ptr(),
-            _addr(ws), sh), "hqq_adapters_backward")
+            dY.data_ptr(), X.data_ptr(), code, M, K, A.data_ptr(), B.data_ptr(), N, rank, n,
+            ids.data_ptr(), scales.data_ptr(), _addr(base), b32, dX.data_ptr(), int(bool(out_f32)),
+            dA.data_ptr(), dB.data_ptr(), _addr(ws), sh), "hqq_adapters_backward")
         return dX, dA, dB
     return _launch(dev, stream, call)
 
@@ -1201,9 +1217,10 @@ def matmul_adapters(X, q: "QuantizedWeight", A, B, ids, scales, out_f32: bool = 
         y = _result(out, (M, N), torch.float32 if out_f32 else torch.float16, dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_adapters(
-            X.data_ptr(), M, K, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N, q.nbits,
-            q.group_size, A.data_ptr(), B.data_ptr(), rank, n, ids.data_ptr(), scales.data_ptr(), y.data_ptr(),
-            int(bool(out_f32)), _addr(ws), sh), "hqq_matmul_adapters")
+            X.data_ptr(), M, K, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N,
+            q.nbits, q.group_size, A.data_ptr(), B.data_ptr(), rank, n, ids.data_ptr(),
+            scales.data_ptr(), y.data_ptr(), int(bool(out_f32)), _addr(ws), sh),
+            "hqq_matmul_adapters")
         return y
     return _launch(dev, stream, call)
 
@@ -1225,9 +1242,9 @@ def matmul_adapters_backward(dY, X, q: "QuantizedWeight", A, B, ids, scales, out
         dB = torch.empty((n, N, rank), dtype=torch.float32, device=dev)
         ws = _scratch(workspace, wb, dev)
         _check_status(hqq_matmul_adapters_backward(
-            dY.data_ptr(), X.data_ptr(), M, K, q.packed.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr(), N, q.nbits,
-            q.group_size, A.data_ptr(), B.data_ptr(), rank, n, ids.data_ptr(), scales.data_ptr(), dX.data_ptr(),
-            int(bool(out_f32)), dA.data_ptr(), dB.data_ptr(), _addr(ws), sh),
-            "hqq_matmul_adapters_backward")
+            dY.data_ptr(), X.data_ptr(), M, K, q.packed.data_ptr(), q.scale.data_ptr(),
+            q.zero.data_ptr(), N, q.nbits, q.group_size, A.data_ptr(), B.data_ptr(), rank, n,
+            ids.data_ptr(), scales.data_ptr(), dX.data_ptr(), int(bool(out_f32)), dA.data_ptr(),
+            dB.data_ptr(), _addr(ws), sh), "hqq_matmul_adapters_backward")
         return dX, dA, dB
     return _launch(dev, stream, call)

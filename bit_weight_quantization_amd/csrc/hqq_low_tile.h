@@ -22,6 +22,8 @@ struct LowRank {
   int rank, adapters;
 };
 
+// The product's accumulators take the sum: no fp32 base goes through memory (with a pass of its own the
+// gradient of 2048 rows, 4096 x 4096, rank 32 took 182 instead of 172 us).
 namespace {
 
 constexpr int kLowRound = 64;                // low-rank values per round

@@ -15,6 +15,9 @@
 namespace hqq {
 namespace {
 
+// The sort is bound by launches and latency: one block sorts up to 4096 slots in 3.3 us (2 slots) to
+// 5 us (4096); beyond, a count and a sort launch: 11 us for 16384 slots of 8 experts, 16 us for 32760
+// of 64.
 constexpr int kSortWaves = 16;
 constexpr int kSortBlock = kSortWaves * kWave;
 constexpr int64_t kSortOneBlock = 4096;  // slots that one block sorts in one launch
@@ -185,7 +188,8 @@ struct Chunk {
 };
 
 // A block per token: every row is read once and written to the topk places of its slots.
-// Bound by HBM: tokens reads and slots writes of a row.
+// Bound by HBM: tokens reads and slots writes of a row (8192 x 4096 binary16, topk 2: 201 MB in
+// 33-35 us, 5.8 TB/s, a part of the writes still in the 256 MB cache)
 template <typename D, bool WIDE>
 __global__ __launch_bounds__(kBlock) void hqq_route_gather_kernel(const RouteRows P) {
   using T = typename D::T;
@@ -210,7 +214,8 @@ __global__ __launch_bounds__(kBlock) void hqq_route_gather_kernel(const RouteRow
 constexpr int kTopkStep = 8;  // choices whose rows are read together
 
 // A block per token: out[t] = sum over its kept choices of weight * row, in fp32 in the order
-// of the choices, rounded once.  The rows of up to 8 choices are in flight together.
+// of the choices, rounded once.  The rows of up to 8 choices are in flight together.  Bound by HBM:
+// 8192 x 4096 binary16 of 2 choices, 201 MB in 48 us, 4.2 TB/s.
 template <typename D, bool WIDE>
 __global__ __launch_bounds__(kBlock) void hqq_route_combine_kernel(const RouteRows P) {
   using T = typename D::T;
@@ -252,7 +257,8 @@ __global__ __launch_bounds__(kBlock) void hqq_route_combine_kernel(const RouteRo
 
 // A block per token: for each kept choice the row's gradient weight * dOut[t] and the
 // weight's gradient <dOut[t], row>; zeros for dropped ones.  The gradient is read once for 8
-// choices, whose dot products meet in a fixed order (butterfly, then the wavefronts).
+// choices, whose dot products meet in a fixed order (butterfly, then the wavefronts).  Bound by HBM:
+// 4095 x 8192 bfloat16 of 8 choices, a tenth dropped, 1.09 GB in 213 us, 5.1 TB/s.
 template <typename D, bool WIDE>
 __global__ __launch_bounds__(kBlock) void hqq_route_combine_backward_kernel(const RouteRows P) {
   using T = typename D::T;
