@@ -203,9 +203,9 @@ struct PairScale {
   float a, c;
 };
 
-// Codes 8 step + 2 e and + 1 of a lane's 32 (LSB first in w) as two binary16 weights.
-template <int NB>
-__device__ __forceinline__ uint32_t decode_pair(const uint32_t (&w)[NB], int step, int e, PairScale p) {
+// Codes 8 step + 2 e and + 1 of a lane's 16 or 32 (LSB first in w) as two binary16 weights.
+template <int NB, int W>
+__device__ __forceinline__ uint32_t decode_pair(const uint32_t (&w)[W], int step, int e, PairScale p) {
   if constexpr (NB == 3) {         // codes straddle bytes: one by one
     const float sv = p.a * (1.f / kSub);
     const float w0 = __builtin_fmaf(sv, (float)code_at<NB>(w, 8 * step + 2 * e), p.c);

@@ -66,13 +66,12 @@ template <int NB, int WM, int ROWS>
 __global__ __launch_bounds__(2 * WM * kWave) __attribute__((amdgpu_waves_per_eu(2)))
 void hqq_matmul_t_kernel(const MatmulTParams P) {
   constexpr int T = 2 * WM * kWave, BM = 64 * WM;
-  constexpr int CB = kTN * kTK / T;  // codes per thread and step
-  static_assert(CB == 16 || CB == 32, "16 or 32 codes of a weight row per thread");
-  constexpr int BP = kTK / CB;       // threads per weight row
-  constexpr int CW = CB == 32 ? NB : Codes16<NB>::kWords;
+  constexpr int CB = 16, BP = kTK / CB;  // codes of a weight row per thread, threads per row
+  constexpr int BR = T / BP, RB = kTN / BR;  // weight rows per round of loads, rounds
+  static_assert(RB == 1 || RB == 2, "one or two weight rows per thread");
   __shared__ __align__(16) _Float16 As[2][BM][kTRowA];
   __shared__ __align__(16) _Float16 Bs[2][kTN][kTRowB];
-  const int tid = threadIdx.x, wid = tid / kWave, lane = tid & (kWave - 1);
+  const int tid = threadIdx.x, wid = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid & (kWave - 1);
   const int wm = wid >> 1, wn = wid & 1;
 
   const int64_t cols = (P.K + kTK - 1) / kTK;
@@ -113,53 +112,48 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
   const int br = tid / BP, bp = tid % BP;
   const int64_t kc = k0 + CB * bp < P.K ? k0 + CB * bp : 0;  // (columns past K are not stored)
   const int64_t row_bytes = (P.K >> 3) * NB, gpr = P.K >> P.group_shift;
-  const int g2 = P.group_size == 16 ? 1 : 0;
 
-  uint4 ar[2][4];
-  uint32_t cw[2][CW];
-  uint32_t s16[2][2], z16[2][2];
-  auto load_global = [&](auto st_const, int64_t step) {
-    constexpr int S = decltype(st_const)::value;
+  uint4 ar[4];
+  uint32_t cw[2][RB][Codes16<NB>::kWords];
+  uint32_t s16[2][RB], z16[2][RB];
+  auto load_rows = [&](int64_t step) {
     const int64_t nb = step * kTN;
     if (nb + kTN <= N) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ar[S][i] = load8(yrow[i] + nb);
+      for (int i = 0; i < 4; ++i) ar[i] = load8(yrow[i] + nb);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ar[S][i] = load8_part(yrow[i] + nb, N - nb - 8 * xp);
-    }
-    const int64_t n = nb + br < N ? nb + br : N - 1;
-    const uint8_t* cp = P.packed + (w0 + n) * row_bytes;
-    if constexpr (CB == 32) load_codes32<NB>(cp + (kc >> 5) * (4 * NB), cw[S]);
-    else load_codes16<NB>(cp + (kc >> 4) * (2 * NB), cw[S]);
-    const int64_t g0 = (w0 + n) * gpr + (kc >> P.group_shift);
-    s16[S][0] = P.scale16[g0];
-    z16[S][0] = P.zero16[g0];
-    if constexpr (CB == 32) {
-      s16[S][1] = P.scale16[g0 + g2];
-      z16[S][1] = P.zero16[g0 + g2];
+      for (int i = 0; i < 4; ++i) ar[i] = load8_part(yrow[i] + nb, N - nb - 8 * xp);
     }
   };
-  auto dequant_b = [&](auto st_const, int64_t step, uint4 (&bv)[CB / 8]) {
+  auto load_codes = [&](auto st_const, int64_t step) {
     constexpr int S = decltype(st_const)::value;
-    const bool ok = step * kTN + br < N;  // rows past N enter as zeros
-    const float s0 = ok ? h2f(s16[S][0]) : 0.f;
-    const float sz0 = ok ? s0 * h2f(z16[S][0]) : 0.f;
-    if constexpr (CB == 32) {
-      const float s1 = ok ? h2f(s16[S][1]) : 0.f;
-      const float sz1 = ok ? s1 * h2f(z16[S][1]) : 0.f;
-      dequant32<NB>(cw[S], s0, sz0, s1, sz1, bv);
-    } else {
-      dequant16<NB>(cw[S], s0, sz0, bv);
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const int64_t m = step * kTN + br + BR * j, n = w0 + (m < N ? m : N - 1);
+      load_codes16<NB>(P.packed + n * row_bytes + (kc >> 4) * (2 * NB), cw[S][j]);
+      const int64_t g = n * gpr + (kc >> P.group_shift);
+      s16[S][j] = P.scale16[g];
+      z16[S][j] = P.zero16[g];
     }
   };
-  auto write_lds = [&](auto st_const, int buf, const uint4 (&bv)[CB / 8]) {
+  auto write_rows = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(&As[buf][xr + T / 8 * i][8 * xp]) = ar[i];
+  };
+  // half of the thread's codes decoded and written; rows past N enter as zeros
+  auto write_weights = [&](auto st_const, int buf, int64_t step, int half) {
     constexpr int S = decltype(st_const)::value;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(&As[buf][xr + T / 8 * i][8 * xp]) = ar[S][i];
-    uint4* bd = reinterpret_cast<uint4*>(&Bs[buf][br][CB * bp]);
-#pragma unroll
-    for (int i = 0; i < CB / 8; ++i) bd[i] = bv[i];
+    for (int u = half * RB; u < (half + 1) * RB; ++u) {  // 8 codes each
+      const int j = u / 2, i = u % 2;
+      const bool ok = step * kTN + br + BR * j < N;
+      const float sv = ok ? h2f(s16[S][j]) : 0.f;
+      const PairScale sc = {sv * kSub, ok ? -sv * h2f(z16[S][j]) : 0.f};
+      *reinterpret_cast<uint4*>(&Bs[buf][br + BR * j][CB * bp + 8 * i]) =
+          make_uint4(decode_pair<NB>(cw[S][j], i, 0, sc), decode_pair<NB>(cw[S][j], i, 1, sc),
+                     decode_pair<NB>(cw[S][j], i, 2, sc), decode_pair<NB>(cw[S][j], i, 3, sc));
+    }
   };
 
   float16_t acc[2][2];
@@ -175,53 +169,95 @@ void hqq_matmul_t_kernel(const MatmulTParams P) {
   // that lanes 4 (l % 4) .. + 4 of the group take: 16 (l & 1) + 4 (2 (a half) + (l & 3) / 2)
   const int tr_row = 8 * (lane >> 5) + ((lane & 15) >> 2);
   const int tr_col = 16 * (lane & 1) + 4 * (2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
-  const bool used0 = wm * 64 < rows;  // wave-uniform
-  auto mfma_step = [&](int buf) {
+  // operands of matrix step ks of a buffer
+  struct Frags {
+    half8_t a[2], b[2];
+  };
+  auto read_frags = [&](int buf, int ks, Frags& f) {
 #pragma unroll
-    for (int ks = 0; ks < kTN / 16; ++ks) {
-      half8_t af[2], bf[2];
+    for (int i = 0; i < 2; ++i)
+      f.a[i] = *reinterpret_cast<const half8_t*>(&As[buf][wm * 64 + i * 32 + (lane & 31)][ks * 16 + (lane >> 5) * 8]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        af[i] = *reinterpret_cast<const half8_t*>(&As[buf][wm * 64 + i * 32 + (lane & 31)][ks * 16 + (lane >> 5) * 8]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const _Float16* src = &Bs[buf][ks * 16 + tr_row][wn * 64 + j * 32 + tr_col];
-        const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)src);
-        const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(src + 4 * kTRowB));
-        bf[j] = __builtin_bit_cast(half8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[j], af[i], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < 2; ++j) {
+      const _Float16* src = &Bs[buf][ks * 16 + tr_row][wn * 64 + j * 32 + tr_col];
+      const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)src);
+      const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(src + 4 * kTRowB));
+      f.b[j] = __builtin_bit_cast(half8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   };
-  auto step = [&](auto st_const, int64_t c) {
-    constexpr int S = decltype(st_const)::value;
-    constexpr std::integral_constant<int, S ^ 1> other{};
-    load_global(st_const, c + 2 < st1 ? c + 2 : st0);
-    uint4 bv[CB / 8];
-    dequant_b(other, c + 1 < st1 ? c + 1 : st0, bv);
-    if (used0) mfma_step(S);  // (a wavefront whose rows are all past the tile only stages)
-    write_lds(other, S ^ 1, bv);  // (after the last step: unused)
-    lds_barrier();
+  auto products = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
   };
-
-  if (st0 < st1) {
+  // One step: four matrix steps, each behind the LDS reads of the next one.  The next tile is written
+  // (its weights decoded) under the first two; the barrier stands before the fourth, whose operands are in
+  // registers by then, so that the next tile's first reads run under it.
+  Frags fr[2];
+  auto step = [&](auto st_const, auto used_const, int64_t c) {
+    constexpr int S = decltype(st_const)::value;
+    constexpr bool USED = decltype(used_const)::value;
+    constexpr std::integral_constant<int, S ^ 1> other{};
+    const int64_t c1 = c + 1 < st1 ? c + 1 : st0, c2 = c + 2 < st1 ? c + 2 : st0;  // (past the end: unused)
+    if constexpr (USED) read_frags(S, 1, fr[1]);
+    write_rows(S ^ 1);
+    load_rows(c2);
+    load_codes(st_const, c2);
+    __builtin_amdgcn_sched_barrier(0);
+    write_weights(other, S ^ 1, c1, 0);
+    if constexpr (USED) products(fr[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (USED) read_frags(S, 2, fr[0]);
+    write_weights(other, S ^ 1, c1, 1);
+    if constexpr (USED) {
+      products(fr[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      read_frags(S, 3, fr[1]);
+      products(fr[0]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    lds_barrier();
+    if constexpr (USED) {
+      read_frags(S ^ 1, 0, fr[0]);
+      products(fr[1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto walk = [&](auto used_const) {
     constexpr std::integral_constant<int, 0> s0{};
     constexpr std::integral_constant<int, 1> s1{};
-    load_global(s0, st0);
-    load_global(s1, st0 + 1 < st1 ? st0 + 1 : st0);
-    uint4 bv[CB / 8];
-    dequant_b(s0, st0, bv);
-    write_lds(s0, 0, bv);
+    const int64_t second = st0 + 1 < st1 ? st0 + 1 : st0;
+    load_rows(st0);
+    load_codes(s0, st0);
+    load_codes(s1, second);
+    write_rows(0);
+    load_rows(second);
+    write_weights(s0, 0, st0, 0);
+    write_weights(s0, 0, st0, 1);
     lds_barrier();
+    if constexpr (decltype(used_const)::value) read_frags(0, 0, fr[0]);
     for (int64_t c = st0; c < st1; c += 2) {
-      step(s0, c);
+      step(s0, used_const, c);
       if (c + 1 >= st1) break;
-      step(s1, c + 1);
+      step(s1, used_const, c + 1);
     }
+  };
+  // a wavefront whose rows are all past the tile only stages (wave-uniform; as many barriers)
+  const bool used = wm * 64 < rows;
+  if constexpr (ROWS != kAdapted) {
+    if (!used) {
+      if (st0 < st1) walk(std::false_type{});
+      return;
+    }
+    if (st0 < st1) walk(std::true_type{});
+  } else {
+    if (st0 < st1) {
+      if (used) walk(std::true_type{});
+      else walk(std::false_type{});
+    }
+    lds_barrier();  // (the buffers are used again below)
   }
 
   float back[2] = {1.f, 1.f};
