@@ -89,6 +89,20 @@ __device__ __forceinline__ short8_t load8(const uint16_t* p, int64_t valid) {
   return v;
 }
 
+// The sum of n values `stride` apart, in order, 8 loads in flight (one by one each add would wait for
+// its load: the second step of 64 rows, 8192 x 8192 of 16 splits took 8.2 us).
+__device__ __forceinline__ float sum_strided(const float* p, int64_t stride, int n) {
+  float y = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i0 + i < n ? p[(i0 + i) * stride] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y += v[i];
+  }
+  return y;
+}
+
 __device__ __forceinline__ float read_base(const AdapterParams& P, int64_t at);
 
 // ---------------------------------------------------------------- few rows --
@@ -141,17 +155,15 @@ __global__ __launch_bounds__(kFewN) void hqq_adapter_expand_few_kernel(const Ada
   const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * kFewN + threadIdx.x;
   const int a = P.ids[m];
   const bool has = (uint32_t)a < (uint32_t)P.adapters;
+  float y = n < P.N ? read_base(P, m * P.N + n) : 0.f;  // (in flight with what follows)
   if (has) {
     const float s = P.scales[a];
     for (int r = threadIdx.x; r < P.rank; r += kFewN) {
-      float t = 0.f;
-      for (int i = 0; i < splits; ++i) t += part[((int64_t)i * P.M + m) * P.rank + r];
-      v[r] = s * t;
+      v[r] = s * sum_strided(part + m * P.rank + r, P.M * P.rank, splits);
     }
   }
   __syncthreads();
   if (n >= P.N) return;
-  float y = read_base(P, m * P.N + n);
   if (has) {
     const uint16_t* b = P.B + ((int64_t)a * P.N + n) * P.rank;
     float t = 0.f;
@@ -169,10 +181,7 @@ __global__ __launch_bounds__(kFewN) void hqq_adapter_expand_few_kernel(const Ada
 __device__ __forceinline__ float read_base(const AdapterParams& P, int64_t at) {
   if (!P.base) return 0.f;
   if (P.base_slabs > 0) {
-    const float* b = static_cast<const float*>(P.base) + at;
-    float y = b[0];
-    for (int i = 1; i < P.base_slabs; ++i) y += b[i * P.base_stride];
-    return y;
+    return sum_strided(static_cast<const float*>(P.base) + at, P.base_stride, P.base_slabs);
   }
   if (P.base_f32) return static_cast<const float*>(P.base)[at];
   const uint16_t v = static_cast<const uint16_t*>(P.base)[at];
