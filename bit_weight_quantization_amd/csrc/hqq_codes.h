@@ -190,12 +190,21 @@ constexpr float kSub = 16777216.f;  // 2^24: a binary16 subnormal's unit is 2^-2
 // binary16 that is a subnormal, q 2^(shift - 24) exactly, and the scales carry the power back.  Two
 // instructions a pair, where conversion in fp32 and a packing conversion take three (and
 // exponents put in front of the codes one more).
+// A matrix instruction must not read d within two wait states of its write, and the compiler, which
+// keeps that distance for its own instructions, does not for these: callers put the result
+// into LDS, or separate it by mfma_distance().
 __device__ __forceinline__ uint32_t weight_pair(uint32_t t, float s_lo, float s_hi, float minus_sz) {
   uint32_t d;
   asm("v_fma_mixlo_f16 %0, %1, %2, %4 op_sel_hi:[1,0,0]\n\t"
       "v_fma_mixhi_f16 %0, %1, %3, %4 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
       : "=&v"(d) : "v"(t), "v"(s_lo), "v"(s_hi), "v"(minus_sz));
   return d;
+}
+
+__device__ __forceinline__ void mfma_distance() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 1");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // A group's scales as decode_pair takes them: s 2^24 and -s z; the other shifts' powers of s.

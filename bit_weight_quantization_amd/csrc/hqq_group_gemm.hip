@@ -217,9 +217,10 @@ void hqq_group_gemm_kernel(const GroupGemmParams P) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s == 2) read_scales(kn, sn);  // (its table was written a barrier ago at least)
+      mfma_distance();
 #pragma unroll
       for (int a = 0; a < TI; ++a) {
-if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
+        if (a < used) {  // uniform: fragments of rows past the tile's cost nothing
 #pragma unroll
           for (int j = 0; j < TJ; ++j)
             acc[a][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
