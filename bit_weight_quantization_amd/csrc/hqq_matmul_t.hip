@@ -6,10 +6,11 @@
 // block into LDS as it is stored (rows n, binary16, as in the forward kernels), and the matrix
 // operand, which needs 8 consecutive n of one k in a lane, is read with gfx950's transposing LDS
 // read (ds_read_b64_tr_b16: of each 16 lanes' 4 x 16 block of halves lane i gets column i).
-// For many rows bound by LDS (a 64 x 64 wavefront tile reads both operands) and the decoding of a
-// weight tile per 128 or 256 rows: 2048 rows, 4096 x 4096 (4 bits) with adapters of rank 32 123 us, 4002
-// rows of 8 such experts 270 us, 500-600 TFLOP/s; dY in 128-byte pieces of a row (8 threads a row)
-// instead of 16-byte ones of 64 rows, and 16 columns a lane in the epilogue, took the first from 150 us.
+// For many rows no unit is busy for more than about a quarter of the time (counters: matrix cores 24%,
+// LDS 24%, VALU 22%): the waits within a step bound it.  2048 rows, 4096 x 4096 (4 bits) with adapters of rank 32 take
+// 105 us (124 with every operand read right before its use), 4002 rows of 8 such experts 250-260 us
+// (280), 530-650 TFLOP/s; dY in 128-byte pieces of a row (8 threads a row) instead of 16-byte ones of
+// 64 rows, and 16 columns a lane in the epilogue, took the first from 150 us.
 // For few rows bound by the latency of one block's walk over n, which is split over blocks and joined
 // in a fixed order (place_tile).
 #include <hip/hip_runtime.h>
@@ -56,8 +57,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {  // 2-byte aligned, 
 
 // (64 WM) x 128 output tile per block of 2 WM wavefronts (64 x 64 each: 2 x 2 tiles of
 // v_mfma_f32_32x32x16_f16), n in steps of 64.  8 threads stage the 128 bytes of a row of dY, and each
-// thread CB codes of one weight row per step.  Pipelined as the forward kernel: loads two steps
-// ahead in registers, LDS double-buffered, one LDS-only barrier per step.  The weight is the A
+// thread 16 codes of one or two weight rows per step (32 of one row, 64 bytes apart in LDS between
+// lanes, cost bank conflicts in 44% of the LDS cycles).  Codes are loaded two steps ahead in registers,
+// LDS is double-buffered, one LDS-only barrier per step.  The weight is the A
 // operand and its row 8 a + 4 h + b stands for column 16 h + 4 a + b of the 32, so that a lane ends
 // with 16 consecutive columns of one row of dX.
 enum Rows : int { kAll = 0, kExperts = 1, kAdapted = 2 };  // rows of one weight, of experts, with adapters
@@ -353,7 +355,7 @@ __global__ __launch_bounds__(kBlock) void hqq_matmul_t_join_kernel(const MatmulT
 
 // Tiles of 256 rows from a mean of 1024 rows an expert on (each weight tile is dequantized once per 256
 // rows), else of 128 (a group's last tile is half full on average: mean 500 rows, 267 us against 284 us
-// with 256).
+// with 256, before the read-ahead).
 int t_wm(int64_t M, int64_t experts) { return M / (experts > 0 ? experts : 1) >= 1024 ? 4 : 2; }
 int64_t t_most(int64_t M, int64_t K, int64_t experts, int64_t bm) {
   return (K + kTK - 1) / kTK * (experts > 0 ? max_row_tiles(M, experts, bm) : (M + bm - 1) / bm);
